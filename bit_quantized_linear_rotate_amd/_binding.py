@@ -78,6 +78,25 @@ _SIGNATURES = {
     "w4a4_linear_bf6_workspace_size": ([_i64, _i64], _sz),
     "w4a4_linear_bf6": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i64, _vp, ctypes.c_int,
                          _vp, _vp, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "w4a4_mx4_scales_size": ([_i64, _i64], _sz),
+    "w4a4_quantize_mx4": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "w4a4_dequantize_mx4": ([_vp, _vp, _i64, _i64, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "w4a4_gemm_mx4": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "w4a4_gemm_mx4_plan": ([_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
+    "w4a4_linear_mx4_workspace_size": ([_i64, _i64], _sz),
+    "w4a4_linear_mx4": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
+                         ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "w4a4_grouped_gemm_mx4": ([_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp,
+                               ctypes.c_int, _vp], ctypes.c_int),
+    "w4a4_grouped_gated_mx4": ([_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp,
+                                _vp, _vp], ctypes.c_int),
+    "w4a4_route_experts_workspace_size": ([_i64, _i32], _sz),
+    "w4a4_route_experts": ([_vp, ctypes.c_int, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                           ctypes.c_int),
+    "w4a4_combine_experts": ([_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp], ctypes.c_int),
+    "w4a4_experts_mx4_workspace_size": ([_i64, _i64, _i64, _i32, _i32, ctypes.c_int], _sz),
+    "w4a4_experts_mx4": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_int, _i64, _i32,
+                          _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "w4a4_linear_noalloc": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i64,
                              _vp, ctypes.c_int, _i32, _vp, _vp, _vp, _i32, _vp, ctypes.c_int, _vp],
                             ctypes.c_int),
@@ -1016,3 +1035,303 @@ def w4a4_linear_bf6(x: torch.Tensor, rot: Optional[torch.Tensor], g: int, w6: to
         _stream(dev))
     _check(rc, "w4a4_linear_bf6")
     return out.view(*lead, N)
+
+
+# ---- MX4 (microscaled 4-bit floating point) -------------------------------------
+
+MX4_KERNELS = {0: "skinny", 1: "tile64", 2: "tile128", 3: "tile256"}
+
+
+def _mx4_slabs(K: int) -> int:
+    return (K + 255) // 256
+
+
+def _mx4_operand(codes, scales, codes_name: str, scales_name: str, lead: int = 0):
+    """Layout check of an MX4 operand (codes (.., rows, K/2), scales (.., slabs,
+    rows, 8), `lead` leading dimensions); returns (rows, K)."""
+    _need(codes, codes_name, dtypes=(torch.uint8,))
+    if codes.dim() != 2 + lead:
+        raise ValueError(f"{codes_name} has shape {tuple(codes.shape)}, expected {2 + lead} dimensions")
+    rows, K = codes.shape[-2], 2 * codes.shape[-1]
+    if K % 32:
+        raise ValueError(f"{codes_name} has shape {tuple(codes.shape)}: K={K} is not a multiple of 32")
+    _need(scales, scales_name, (*codes.shape[:lead], _mx4_slabs(K), rows, 8), (torch.uint8,))
+    return rows, K
+
+
+def _mx4_act(x, h, K: int):
+    """(group size, sign_in, sign_out) of an optional Hadamard rotation."""
+    if K % 32:
+        raise ValueError(f"K={K} is not a multiple of 32")
+    if h is None:
+        return 0, None, None
+    _hadamard_arg(h)
+    if K % h.g:
+        raise ValueError(f"K={K} is not a multiple of g={h.g}")
+    return h.g, h.sign_in, h.sign_out
+
+
+def _workspace(workspace, need: int, dev):
+    if workspace is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", dtypes=(torch.uint8,))
+    if workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes, need {need}")
+    return workspace
+
+
+def w4a4_quantize_mx4(x: torch.Tensor, h: Optional[Hadamard] = None):
+    """Rows of x (..., K) to MX4, rotated by h first if given.  Returns (codes
+    uint8 (M, K/2), scales uint8 (ceil(K/256), M, 8)).  K % 32 == 0.  Weights
+    (N, K) are quantized by the same call; E experts' weights (E, N, K) per
+    expert, or through mx4_scales_from_rows."""
+    x2 = _as_2d(_need(x, "x", contiguous=False))
+    M, K = x2.shape
+    dt = _dt(x2)
+    g, si, so = _mx4_act(x2, h, K)
+    _same_device(x2, sign_in=si, sign_out=so)
+    dev = x2.device
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((_mx4_slabs(K), M, 8), dtype=torch.uint8, device=dev)
+    rc = lib().w4a4_quantize_mx4(_ptr(x2), dt, M, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(codes),
+                                 _ptr(scales), _stream(dev))
+    _check(rc, "w4a4_quantize_mx4")
+    return codes, scales
+
+
+def w4a4_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values (M, K) that MX4 codes and scales stand for."""
+    M, K = _mx4_operand(codes, scales, "codes", "scales")
+    if dtype not in _FLOAT:
+        raise ValueError(f"dtype {dtype} is not float32/float16/bfloat16")
+    _same_device(codes, scales=scales)
+    out = torch.empty((M, K), dtype=dtype, device=codes.device)
+    rc = lib().w4a4_dequantize_mx4(_ptr(codes), _ptr(scales), M, K, _ptr(out), _DT[dtype], _stream(codes.device))
+    _check(rc, "w4a4_dequantize_mx4")
+    return out
+
+
+def mx4_scales_from_rows(scales: torch.Tensor) -> torch.Tensor:
+    """Scale bytes in rows (..., rows, K/32) -> slabs (..., ceil(K/256), rows, 8),
+    the layout the MX4 calls take (weights stored elsewhere; once per layer)."""
+    _need(scales, "scales", dtypes=(torch.uint8,), contiguous=False)
+    s = torch.nn.functional.pad(scales, (0, -scales.shape[-1] % 8))
+    return s.reshape(*s.shape[:-1], s.shape[-1] // 8, 8).transpose(-3, -2).contiguous()
+
+
+def mx4_scales_to_rows(scales: torch.Tensor, K: int) -> torch.Tensor:
+    """The inverse of mx4_scales_from_rows: (..., rows, K/32)."""
+    _need(scales, "scales", dtypes=(torch.uint8,), contiguous=False)
+    s = scales.transpose(-3, -2)
+    return s.reshape(*s.shape[:-2], -1)[..., :K // 32].contiguous()
+
+
+def w4a4_gemm_mx4_plan(rows: int, K: int, N: int, experts: int = 0, gated: bool = False) -> str:
+    """Name of the kernel an MX4 product of `rows` rows takes (experts = 0: dense)."""
+    k = ctypes.c_int(-1)
+    _check(lib().w4a4_gemm_mx4_plan(rows, K, N, experts, int(gated), ctypes.byref(k)), "w4a4_gemm_mx4_plan")
+    return MX4_KERNELS.get(k.value, "none")
+
+
+def w4a4_gemm_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                  bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The MX4 product: (M, N) from activations and weights (N, K) in MX4."""
+    M, K = _mx4_operand(codes, scales, "codes", "scales")
+    N, Kw = _mx4_operand(w_codes, w_scales, "w_codes", "w_scales")
+    if Kw != K:
+        raise ValueError(f"w_codes has shape {tuple(w_codes.shape)}, expected (N, {K // 2})")
+    if bias is not None:
+        _need(bias, "bias", (N,), _FLOAT)
+    if out_dtype not in _FLOAT:
+        raise ValueError(f"out_dtype {out_dtype} is not float32/float16/bfloat16")
+    _same_device(codes, scales=scales, w_codes=w_codes, w_scales=w_scales, bias=bias)
+    out = torch.empty((M, N), dtype=out_dtype, device=codes.device)
+    rc = lib().w4a4_gemm_mx4(_ptr(codes), _ptr(scales), M, K, _ptr(w_codes), _ptr(w_scales), N, _ptr(bias),
+                             _dt(bias) if bias is not None else 0, _ptr(out), _DT[out_dtype], _stream(codes.device))
+    _check(rc, "w4a4_gemm_mx4")
+    return out
+
+
+def w4a4_linear_mx4_workspace_size(M: int, K: int) -> int:
+    return int(lib().w4a4_linear_mx4_workspace_size(M, K))
+
+
+def w4a4_linear_mx4(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, h: Optional[Hadamard] = None,
+                    bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The linear layer on MX4: x (..., K) is quantized (rotated by h first if
+    given) and multiplied by weights (N, K) in MX4."""
+    lead = _need(x, "x", contiguous=False).shape[:-1]
+    x2 = _as_2d(x)
+    M, K = x2.shape
+    dt = _dt(x2)
+    g, si, so = _mx4_act(x2, h, K)
+    N, Kw = _mx4_operand(w_codes, w_scales, "w_codes", "w_scales")
+    if Kw != K:
+        raise ValueError(f"w_codes has shape {tuple(w_codes.shape)}, expected (N, {K // 2})")
+    if bias is not None:
+        _need(bias, "bias", (N,), (x2.dtype,))
+    out_dtype = out_dtype or (out.dtype if out is not None else x2.dtype)
+    if out_dtype not in _FLOAT:
+        raise ValueError(f"out_dtype {out_dtype} is not float32/float16/bfloat16")
+    if out is not None:
+        _need(out, "out", (M, N), (out_dtype,))
+    _same_device(x2, sign_in=si, sign_out=so, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out,
+                 workspace=workspace)
+    dev = x2.device
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    workspace = _workspace(workspace, w4a4_linear_mx4_workspace_size(M, K), dev)
+    rc = lib().w4a4_linear_mx4(_ptr(x2), dt, M, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(w_codes),
+                               _ptr(w_scales), N, _ptr(bias), _ptr(out), _DT[out_dtype], _ptr(workspace),
+                               workspace.numel(), _stream(dev))
+    _check(rc, "w4a4_linear_mx4")
+    return out.view(*lead, N)
+
+
+# ---- products grouped by expert --------------------------------------------------
+
+def _grouped_checks(codes, scales, w_codes, w_scales, offsets, rows, bias, gated=False):
+    """Validation shared by the grouped products; returns (M, K, E, N, R)."""
+    M, K = _mx4_operand(codes, scales, "codes", "scales")
+    N, Kw = _mx4_operand(w_codes, w_scales, "w_codes", "w_scales", 1)
+    E = w_codes.shape[0]
+    if Kw != K:
+        raise ValueError(f"w_codes has shape {tuple(w_codes.shape)}, expected (E, N, {K // 2})")
+    if gated and N % 64:
+        raise ValueError(f"w_codes has {N} rows per expert: gates and ups come in blocks of 32")
+    _need(offsets, "offsets", (E + 1,), (torch.int32,))
+    R = M
+    if rows is not None:
+        _need(rows, "rows", dtypes=(torch.int32,))
+        if rows.dim() != 1:
+            raise ValueError(f"rows has shape {tuple(rows.shape)}, expected (R,)")
+        R = rows.shape[0]
+    if bias is not None:
+        _need(bias, "bias", (E, N), _FLOAT)
+    _same_device(codes, scales=scales, w_codes=w_codes, w_scales=w_scales, offsets=offsets, rows=rows, bias=bias)
+    return M, K, E, N, R
+
+
+def w4a4_grouped_gemm_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                          offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                          bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """MX4 products grouped by expert: sorted row i (of expert e's
+    offsets[e] .. offsets[e + 1] - 1; int32 (E + 1,) on the device) is row
+    rows[i] of codes (rows None: row i) and meets expert e's weights (E, N, K).
+    Returns (R, N); rows from offsets[E] on are zeros."""
+    M, K, E, N, R = _grouped_checks(codes, scales, w_codes, w_scales, offsets, rows, bias)
+    if out_dtype not in _FLOAT:
+        raise ValueError(f"out_dtype {out_dtype} is not float32/float16/bfloat16")
+    dev = codes.device
+    out = torch.empty((R, N), dtype=out_dtype, device=dev)
+    rc = lib().w4a4_grouped_gemm_mx4(_ptr(codes), _ptr(scales), M, K, _ptr(w_codes), _ptr(w_scales), E, N,
+                                     _ptr(offsets), _ptr(rows), R, _ptr(bias), _dt(bias) if bias is not None else 0,
+                                     _ptr(out), _DT[out_dtype], _stream(dev))
+    _check(rc, "w4a4_grouped_gemm_mx4")
+    return out
+
+
+def w4a4_grouped_gated_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                           offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None):
+    """The grouped product with weights (E, 2 F, K), F gates then F ups: the MX4
+    form (codes (R, F/2), scales (ceil(F/256), R, 8)) of silu(gate) * up."""
+    M, K, E, N, R = _grouped_checks(codes, scales, w_codes, w_scales, offsets, rows, bias, True)
+    dev = codes.device
+    out_codes = torch.empty((R, N // 4), dtype=torch.uint8, device=dev)
+    out_scales = torch.empty((_mx4_slabs(N // 2), R, 8), dtype=torch.uint8, device=dev)
+    rc = lib().w4a4_grouped_gated_mx4(_ptr(codes), _ptr(scales), M, K, _ptr(w_codes), _ptr(w_scales), E, N,
+                                      _ptr(offsets), _ptr(rows), R, _ptr(bias), _dt(bias) if bias is not None else 0,
+                                      _ptr(out_codes), _ptr(out_scales), _stream(dev))
+    _check(rc, "w4a4_grouped_gated_mx4")
+    return out_codes, out_scales
+
+
+def w4a4_route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = True):
+    """Top-k routing of logits (T, E): (weights fp32 (T, k), experts int32 (T, k),
+    rows int32 (T k,), pos int32 (T, k), offsets int32 (E + 1,)).  Equal logits
+    go to the lower index; NaN and -inf logits are never taken (expert and pos
+    -1, weight 0).  rows and offsets are what the grouped products take, pos and
+    weights what w4a4_combine_experts takes."""
+    _need(logits, "logits", contiguous=False)
+    dt = _dt(logits)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError(f"logits must be (T, E) with contiguous rows, got shape {tuple(logits.shape)}")
+    T, E = logits.shape
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k={top_k} of {E} experts")
+    _same_device(logits)
+    dev = logits.device
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    experts = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    rows = torch.empty((T * top_k,), dtype=torch.int32, device=dev)
+    pos = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    need = int(lib().w4a4_route_experts_workspace_size(T, E))
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    rc = lib().w4a4_route_experts(_ptr(logits), dt, T, logits.stride(0), E, top_k, int(bool(renormalize)),
+                                  _ptr(weights), _ptr(experts), _ptr(rows), _ptr(pos), _ptr(offsets), _ptr(ws), need,
+                                  _stream(dev))
+    _check(rc, "w4a4_route_experts")
+    return weights, experts, rows, pos, offsets
+
+
+def w4a4_combine_experts(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[pos[t, j]] (pos -1 adds nothing), (T, N) in y's dtype."""
+    _need(y, "y", dtypes=_FLOAT)
+    _need(pos, "pos", dtypes=(torch.int32,))
+    if y.dim() != 2 or pos.dim() != 2 or pos.shape[1] < 1:
+        raise ValueError(f"y {tuple(y.shape)} and pos {tuple(pos.shape)} must be (R, N) and (T, k)")
+    _need(weights, "weights", tuple(pos.shape), (torch.float32,))
+    _same_device(y, pos=pos, weights=weights)
+    R, N = y.shape
+    T, k = pos.shape
+    out = torch.empty((T, N), dtype=y.dtype, device=y.device)
+    rc = lib().w4a4_combine_experts(_ptr(y), _DT[y.dtype], R, N, _ptr(pos), _ptr(weights), T, k, _ptr(out),
+                                    _stream(y.device))
+    _check(rc, "w4a4_combine_experts")
+    return out
+
+
+def w4a4_experts_mx4_workspace_size(T: int, K: int, F: int, E: int, top_k: int, dtype: torch.dtype) -> int:
+    return int(lib().w4a4_experts_mx4_workspace_size(T, K, F, E, top_k, _DT[dtype]))
+
+
+def w4a4_experts_mx4(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_codes: torch.Tensor,
+                     w13_scales: torch.Tensor, w2_codes: torch.Tensor, w2_scales: torch.Tensor,
+                     h: Optional[Hadamard] = None, renormalize: bool = True,
+                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The expert layer on x (..., K) with router logits (T, E): route, quantize
+    (rotated by h first if given), gated product with w13 (E, 2 F, K; F gates
+    then F ups), product with w2 (E, K, F), weighted sum per token."""
+    lead = _need(x, "x", contiguous=False).shape[:-1]
+    x2 = _as_2d(x)
+    T, K = x2.shape
+    dt = _dt(x2)
+    g, si, so = _mx4_act(x2, h, K)
+    N1, K1 = _mx4_operand(w13_codes, w13_scales, "w13_codes", "w13_scales", 1)
+    N2, F = _mx4_operand(w2_codes, w2_scales, "w2_codes", "w2_scales", 1)
+    E = w13_codes.shape[0]
+    if K1 != K or N1 != 2 * F or N2 != K or w2_codes.shape[0] != E:
+        raise ValueError(f"w13_codes {tuple(w13_codes.shape)} and w2_codes {tuple(w2_codes.shape)} must be "
+                         f"(E, 2 F, {K // 2}) and (E, {K}, F/2)")
+    _need(logits, "logits", (T, E), _FLOAT, contiguous=False)
+    if logits.stride(1) != 1 and E > 1:
+        raise ValueError("logits must have contiguous rows")
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k={top_k} of {E} experts")
+    if out is not None:
+        _need(out, "out", (T, K), (x2.dtype,))
+    _same_device(x2, sign_in=si, sign_out=so, logits=logits, w13_codes=w13_codes, w13_scales=w13_scales,
+                 w2_codes=w2_codes, w2_scales=w2_scales, workspace=workspace, out=out)
+    dev = x2.device
+    if out is None:
+        out = torch.empty((T, K), dtype=x2.dtype, device=dev)
+    workspace = _workspace(workspace, int(lib().w4a4_experts_mx4_workspace_size(T, K, F, E, top_k, dt)), dev)
+    rc = lib().w4a4_experts_mx4(
+        _ptr(x2), dt, T, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(logits), _DT[logits.dtype],
+        logits.stride(0), E, top_k, int(bool(renormalize)), _ptr(w13_codes), _ptr(w13_scales), F, _ptr(w2_codes),
+        _ptr(w2_scales), _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev))
+    _check(rc, "w4a4_experts_mx4")
+    return out.view(*lead, K)

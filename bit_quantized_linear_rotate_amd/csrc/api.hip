@@ -10,6 +10,7 @@
 
 #include "../../include/w4a4.h"
 #include "kernels.hpp"
+#include "mx4.hpp"
 
 using namespace w4a4;
 
@@ -127,6 +128,146 @@ int gemm_validate(const int8_t* codes, const float* scales, int64_t M, int64_t K
     }
     return W4A4_OK;
 }
+
+// ---- MX4 arguments -------------------------------------------------------
+constexpr int64_t kMxMaxK = (int64_t)1 << 24;      // a row of codes spans at most 8 MB
+constexpr int64_t kMxMaxRows = (int64_t)1 << 28;   // rows of a scale slab stay below 2^31 bytes
+
+int mx4_shape(int64_t rows, int64_t K, const char* what)
+{
+    if (rows < 0 || K < 0) return fail(W4A4_INVALID, "negative size (%s)", what);
+    if (K % kMxBlock) return fail(W4A4_INVALID, "K=%lld is not a multiple of 32 (%s)", (long long)K, what);
+    if (rows > 0 && K == 0) return fail(W4A4_INVALID, "K=0 with rows (%s)", what);
+    if (K > kMxMaxK || rows > kMxMaxRows)
+        return fail(W4A4_UNSUPPORTED, "%lld rows of %lld values: at most 2^28 and 2^24 (%s)", (long long)rows, (long long)K,
+                    what);
+    return W4A4_OK;
+}
+
+int mx4_operand(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, const char* what)
+{
+    int rc = mx4_shape(rows, K, what);
+    if (rc) return rc;
+    if (rows > 0 && (!codes || !scales)) return fail(W4A4_INVALID, "codes/scales is NULL (%s)", what);
+    if ((uintptr_t)codes % 16 || (uintptr_t)scales % 4)
+        return fail(W4A4_UNSUPPORTED, "codes must be 16-byte and scales 4-byte aligned (%s)", what);
+    return W4A4_OK;
+}
+
+size_t mx4_codes_bytes(int64_t rows, int64_t K) { return rows > 0 && K > 0 ? (size_t)rows * (size_t)(K / 2) : 0; }
+size_t mx4_scales_bytes(int64_t rows, int64_t K)
+{
+    return rows > 0 && K > 0 ? (size_t)mx4_slabs(K) * (size_t)rows * 8 : 0;
+}
+
+int mx4_quant_validate(const void* x, int x_dtype, int64_t M, int64_t K, int64_t sm, int64_t sk, int32_t g,
+                       const int8_t* sign_in, const int8_t* sign_out)
+{
+    int rc = check_activation(x, x_dtype, M, K, sm, sk, false);
+    if (rc) return rc;
+    rc = mx4_shape(M, K, "x");
+    if (rc) return rc;
+    if (g < 0) return fail(W4A4_INVALID, "group size g=%d", g);
+    if (g == 0) return W4A4_OK;
+    if (!pow2_g(g)) return fail(W4A4_UNSUPPORTED, "g=%d is not a power of two in [16, 256]", g);
+    if (K % g) return fail(W4A4_INVALID, "K=%lld is not a multiple of g=%d", (long long)K, g);
+    if ((uintptr_t)sign_in % 8 || (uintptr_t)sign_out % 8)
+        return fail(W4A4_UNSUPPORTED, "sign_in and sign_out must be 8-byte aligned");
+    return W4A4_OK;
+}
+
+int mx4_gemm_validate(const Mx4GemmArgs& a)
+{
+    int rc = mx4_operand(a.a, a.sa, a.M, a.K, "activations");
+    if (rc) return rc;
+    if (a.N < 0) return fail(W4A4_INVALID, "negative size");
+    rc = mx4_operand(a.b, a.sb, a.N, a.K, "weights");
+    if (rc) return rc;
+    const bool gated = a.out_codes || a.out_scales;
+    if ((!gated && !dtype_ok(a.out_dtype)) || (a.bias && !dtype_ok(a.bias_dtype)))
+        return fail(W4A4_UNSUPPORTED, "unknown dtype code");
+    const int64_t rows = a.E ? a.R : a.M;
+    if (rows > 0 && a.N > 0 && !gated && !a.out) return fail(W4A4_INVALID, "out is NULL");
+    // tiles of 64 rows and 256 columns at the least: the grid stays below 2^31 threads
+    if ((rows / 64 + a.E + 1) * (a.N / 128 + 1) >= (int64_t)1 << 23)
+        return fail(W4A4_UNSUPPORTED, "an output of %lld x %lld is too large for one call", (long long)rows, (long long)a.N);
+    return W4A4_OK;
+}
+
+int mx4_grouped_validate(const Mx4GemmArgs& a)
+{
+    if (a.E < 1) return fail(W4A4_INVALID, "E=%d experts", a.E);
+    if (a.R < 0) return fail(W4A4_INVALID, "negative size");
+    if (a.R >= (int64_t)1 << 31) return fail(W4A4_UNSUPPORTED, "%lld sorted rows: at most 2^31 - 1", (long long)a.R);
+    int rc = mx4_gemm_validate(a);
+    if (rc) return rc;
+    if (a.R > 0 && !a.offsets) return fail(W4A4_INVALID, "offsets is NULL");
+    if (!a.rows && a.M != a.R)
+        return fail(W4A4_INVALID, "%lld rows of codes for %lld sorted rows and no row index", (long long)a.M, (long long)a.R);
+    if (a.rows && a.M * (a.K / 2) > (int64_t)1 << 31)
+        return fail(W4A4_UNSUPPORTED, "codes of more than 2^31 bytes behind a row index");
+    return W4A4_OK;
+}
+
+int mx4_gated_validate(const Mx4GemmArgs& a)
+{
+    if (a.N % (2 * kMxBlock))
+        return fail(W4A4_INVALID, "N=%lld: gates and ups come in blocks of 32, N in multiples of 64", (long long)a.N);
+    int rc = mx4_grouped_validate(a);
+    if (rc) return rc;
+    if (a.R > 0 && a.N > 0 && (!a.out_codes || !a.out_scales)) return fail(W4A4_INVALID, "out_codes/out_scales is NULL");
+    if ((uintptr_t)a.out_codes % 16 || (uintptr_t)a.out_scales % 4)
+        return fail(W4A4_UNSUPPORTED, "out_codes must be 16-byte and out_scales 4-byte aligned");
+    return W4A4_OK;
+}
+
+int route_validate(const RouteArgs& a)
+{
+    if (a.T < 0) return fail(W4A4_INVALID, "negative size");
+    if (!dtype_ok(a.dtype)) return fail(W4A4_UNSUPPORTED, "unknown dtype code %d", a.dtype);
+    if (a.E < 1 || a.k < 1 || a.k > a.E) return fail(W4A4_INVALID, "top_k=%d of E=%d experts", a.k, a.E);
+    if (a.E > kRouteMaxExperts || a.k > kRouteMaxTopK)
+        return fail(W4A4_UNSUPPORTED, "E=%d, top_k=%d: at most %d and %d", a.E, a.k, kRouteMaxExperts, kRouteMaxTopK);
+    if (a.stride < a.E && a.T > 1) return fail(W4A4_INVALID, "logits rows overlap (stride %lld)", (long long)a.stride);
+    if (a.T * a.k >= (int64_t)1 << 31) return fail(W4A4_UNSUPPORTED, "T top_k = %lld: at most 2^31 - 1", (long long)(a.T * a.k));
+    if (!a.offsets) return fail(W4A4_INVALID, "offsets is NULL");
+    if (a.T > 0 && (!a.logits || !a.weights || !a.experts || !a.rows || !a.pos))
+        return fail(W4A4_INVALID, "a required pointer is NULL");
+    return W4A4_OK;
+}
+
+size_t route_bytes(int64_t T, int E)
+{
+    const int64_t c = T > 0 ? route_chunks(T) : 1;
+    return c > 1 ? (size_t)c * (size_t)E * 4 : 0;
+}
+
+// the expert layer's workspace, in order
+struct ExpertsSpace {
+    size_t hist, weights, experts, rows, pos, offsets, codes, scales, act_codes, act_scales, y, total;
+    ExpertsSpace(int64_t T, int64_t K, int64_t F, int E, int k, int dtype)
+    {
+        const int64_t R = T * k;
+        size_t at = 0;
+        auto take = [&](size_t bytes) {
+            const size_t here = at;
+            at += align256(bytes);
+            return here;
+        };
+        hist = take(route_bytes(T, E));
+        weights = take((size_t)R * 4);
+        experts = take((size_t)R * 4);
+        rows = take((size_t)R * 4);
+        pos = take((size_t)R * 4);
+        offsets = take((size_t)(E + 1) * 4);
+        codes = take(mx4_codes_bytes(T, K));
+        scales = take(mx4_scales_bytes(T, K));
+        act_codes = take(mx4_codes_bytes(R, F));
+        act_scales = take(mx4_scales_bytes(R, F));
+        y = take((size_t)R * (size_t)K * dsize(dtype));
+        total = at;
+    }
+};
 
 // Scratch of w4a4_linear_noalloc: the codes, scales, low-rank activations
 // and (for very long K) int64 partial sums of one call.  Each GPU the library
@@ -848,6 +989,235 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
     if (e != hipSuccess) return hip_fail(e, "bf6 encoder launch");
     e = launch_gemm_bf6(ga, st);
     return e == hipSuccess ? W4A4_OK : hip_fail(e, "bf6 gemm launch");
+}
+
+// ---- MX4 (microscaled 4-bit floating point) ---------------------------------
+
+size_t w4a4_mx4_scales_size(int64_t rows, int64_t K) { return mx4_scales_bytes(rows, K); }
+
+int w4a4_quantize_mx4(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                      const int8_t* sign_in, const int8_t* sign_out, uint8_t* codes, uint8_t* scales, void* stream)
+{
+    int rc = mx4_quant_validate(x, x_dtype, M, K, stride_m, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    rc = mx4_operand(codes, scales, M, K, "codes");
+    if (rc || M == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const Mx4QuantArgs a{x, x_dtype, M, K, stride_m, stride_k, g, sign_in, sign_out, codes, scales};
+    const hipError_t e = launch_mx4_quantize(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "mx4 quantizer launch");
+}
+
+int w4a4_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out, int out_dtype,
+                        void* stream)
+{
+    int rc = mx4_operand(codes, scales, M, K, "codes");
+    if (rc) return rc;
+    if (!dtype_ok(out_dtype)) return fail(W4A4_UNSUPPORTED, "unknown dtype code %d", out_dtype);
+    if (M > 0 && !out) return fail(W4A4_INVALID, "out is NULL");
+    if ((uintptr_t)out % 16) return fail(W4A4_UNSUPPORTED, "out must be 16-byte aligned");
+    if (M == 0) return W4A4_OK;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_mx4_dequantize(codes, scales, M, K, out, out_dtype, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "mx4 dequantizer launch");
+}
+
+int w4a4_gemm_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, const uint8_t* w_codes,
+                  const uint8_t* w_scales, int64_t N, const void* bias, int bias_dtype, void* out, int out_dtype,
+                  void* stream)
+{
+    const Mx4GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    int rc = mx4_gemm_validate(a);
+    if (rc || M == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_mx4_gemm(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "mx4 gemm launch");
+}
+
+int w4a4_gemm_mx4_plan(int64_t rows, int64_t K, int64_t N, int32_t E, int32_t gated, int* kernel)
+{
+    if (!kernel) return fail(W4A4_INVALID, "kernel is NULL");
+    if (E < 0 || (gated && !E)) return fail(W4A4_INVALID, "E=%d experts", E);
+    int rc = mx4_shape(rows, K, "activations");
+    if (rc) return rc;
+    rc = mx4_shape(N, K, "weights");
+    if (rc) return rc;
+    Mx4GemmArgs a{nullptr, nullptr, rows, K, N, nullptr, nullptr, nullptr, 0, nullptr, W4A4_BF16};
+    a.E = E;
+    a.R = rows;
+    if (gated) a.out_codes = (uint8_t*)16;
+    *kernel = rows == 0 || N == 0 ? -1 : mx4_gemm_path(a);
+    return W4A4_OK;
+}
+
+size_t w4a4_linear_mx4_workspace_size(int64_t M, int64_t K)
+{
+    return M > 0 && K > 0 ? align256(mx4_codes_bytes(M, K)) + align256(mx4_scales_bytes(M, K)) : 0;
+}
+
+int w4a4_linear_mx4(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                    const int8_t* sign_in, const int8_t* sign_out, const uint8_t* w_codes, const uint8_t* w_scales,
+                    int64_t N, const void* bias, void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                    void* stream)
+{
+    int rc = mx4_quant_validate(x, x_dtype, M, K, stride_m, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    uint8_t* codes = (uint8_t*)workspace;
+    uint8_t* scales = codes + align256(mx4_codes_bytes(M, K));
+    const Mx4GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, x_dtype, out, out_dtype};
+    if (M > 0 && N > 0 && (!workspace || workspace_bytes < w4a4_linear_mx4_workspace_size(M, K)))
+        return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, w4a4_linear_mx4_workspace_size(M, K));
+    if (M == 0 || N == 0) return N < 0 ? fail(W4A4_INVALID, "negative size") : W4A4_OK;
+    rc = mx4_gemm_validate(a);
+    if (rc) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    hipStream_t st = (hipStream_t)stream;
+    const Mx4QuantArgs qa{x, x_dtype, M, K, stride_m, stride_k, g, sign_in, sign_out, codes, scales};
+    hipError_t e = launch_mx4_quantize(qa, st);
+    if (e != hipSuccess) return hip_fail(e, "mx4 quantizer launch");
+    e = launch_mx4_gemm(a, st);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "mx4 gemm launch");
+}
+
+int w4a4_grouped_gemm_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, const uint8_t* w_codes,
+                          const uint8_t* w_scales, int32_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
+                          int64_t R, const void* bias, int bias_dtype, void* out, int out_dtype, void* stream)
+{
+    Mx4GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    a.E = E;
+    a.R = R;
+    a.offsets = offsets;
+    a.rows = rows;
+    int rc = mx4_grouped_validate(a);
+    if (rc || R == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_mx4_gemm(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "mx4 grouped gemm launch");
+}
+
+int w4a4_grouped_gated_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, const uint8_t* w_codes,
+                           const uint8_t* w_scales, int32_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
+                           int64_t R, const void* bias, int bias_dtype, uint8_t* out_codes, uint8_t* out_scales,
+                           void* stream)
+{
+    Mx4GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, nullptr, W4A4_BF16};
+    a.E = E;
+    a.R = R;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.out_codes = out_codes;
+    a.out_scales = out_scales;
+    if (R > 0 && N > 0 && (!out_codes || !out_scales)) return fail(W4A4_INVALID, "out_codes/out_scales is NULL");
+    int rc = mx4_gated_validate(a);
+    if (rc || R == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_mx4_gemm(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "mx4 gated grouped gemm launch");
+}
+
+size_t w4a4_route_experts_workspace_size(int64_t T, int32_t E) { return T > 0 && E > 0 ? route_bytes(T, E) : 0; }
+
+int w4a4_route_experts(const void* logits, int dtype, int64_t T, int64_t stride, int32_t E, int32_t top_k,
+                       int32_t renormalize, float* weights, int32_t* experts, int32_t* rows, int32_t* pos,
+                       int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const RouteArgs a{logits, dtype, T, stride, E, top_k, renormalize, weights, experts, rows, pos, offsets,
+                      (int32_t*)workspace};
+    int rc = route_validate(a);
+    if (rc) return rc;
+    const size_t need = w4a4_route_experts_workspace_size(T, E);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_route(a, (hipStream_t)stream);   // (T = 0: the offsets are still written)
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "routing launch");
+}
+
+int w4a4_combine_experts(const void* y, int dtype, int64_t R, int64_t N, const int32_t* pos, const float* weights,
+                         int64_t T, int32_t top_k, void* out, void* stream)
+{
+    if (R < 0 || N < 0 || T < 0) return fail(W4A4_INVALID, "negative size");
+    if (!dtype_ok(dtype)) return fail(W4A4_UNSUPPORTED, "unknown dtype code %d", dtype);
+    if (top_k < 1) return fail(W4A4_INVALID, "top_k=%d", top_k);
+    if (R >= (int64_t)1 << 31) return fail(W4A4_UNSUPPORTED, "%lld sorted rows: at most 2^31 - 1", (long long)R);
+    if (T == 0 || N == 0) return W4A4_OK;
+    if ((R > 0 && !y) || !pos || !weights || !out) return fail(W4A4_INVALID, "a required pointer is NULL");
+    const int rc = device_check();
+    if (rc) return rc;
+    const CombineArgs a{y, dtype, R, T, N, top_k, pos, weights, out};
+    const hipError_t e = launch_combine(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "combining launch");
+}
+
+size_t w4a4_experts_mx4_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k, int x_dtype)
+{
+    if (T <= 0 || K <= 0 || F <= 0 || E <= 0 || top_k <= 0 || !dtype_ok(x_dtype)) return 0;
+    return ExpertsSpace(T, K, F, E, top_k, x_dtype).total;
+}
+
+int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                     const int8_t* sign_in, const int8_t* sign_out, const void* logits, int logits_dtype,
+                     int64_t logits_stride, int32_t E, int32_t top_k, int32_t renormalize, const uint8_t* w13_codes,
+                     const uint8_t* w13_scales, int64_t F, const uint8_t* w2_codes, const uint8_t* w2_scales, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = mx4_quant_validate(x, x_dtype, T, K, stride_m, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    if (F < 1 || F % kMxBlock) return fail(W4A4_INVALID, "F=%lld is not a positive multiple of 32", (long long)F);
+    if (E < 1 || top_k < 1 || top_k > E) return fail(W4A4_INVALID, "top_k=%d of E=%d experts", top_k, E);
+    if (T == 0) return W4A4_OK;
+    if (T * top_k >= (int64_t)1 << 28)
+        return fail(W4A4_UNSUPPORTED, "T top_k = %lld: at most 2^28 - 1", (long long)(T * top_k));
+    const ExpertsSpace at(T, K, F, E, top_k, x_dtype);
+    if (!workspace || workspace_bytes < at.total)
+        return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, at.total);
+    if ((uintptr_t)workspace % 16) return fail(W4A4_UNSUPPORTED, "the workspace must be 16-byte aligned");
+    if (!out) return fail(W4A4_INVALID, "out is NULL");
+    uint8_t* ws = (uint8_t*)workspace;
+    float* weights = (float*)(ws + at.weights);
+    int32_t *rows = (int32_t*)(ws + at.rows), *pos = (int32_t*)(ws + at.pos), *offsets = (int32_t*)(ws + at.offsets);
+    const int64_t R = T * top_k;
+    const RouteArgs ra{logits, logits_dtype, T, logits_stride, E, top_k, renormalize, weights, (int32_t*)(ws + at.experts),
+                       rows, pos, offsets, (int32_t*)(ws + at.hist)};
+    rc = route_validate(ra);
+    if (rc) return rc;
+    const Mx4QuantArgs qa{x, x_dtype, T, K, stride_m, stride_k, g, sign_in, sign_out, ws + at.codes, ws + at.scales};
+    Mx4GemmArgs g1{qa.codes, qa.scales, T, K, 2 * F, w13_codes, w13_scales, nullptr, 0, nullptr, W4A4_BF16};
+    g1.E = E;
+    g1.R = R;
+    g1.offsets = offsets;
+    g1.rows = rows;
+    g1.out_codes = ws + at.act_codes;
+    g1.out_scales = ws + at.act_scales;
+    rc = mx4_gated_validate(g1);
+    if (rc) return rc;
+    Mx4GemmArgs g2{g1.out_codes, g1.out_scales, R, F, K, w2_codes, w2_scales, nullptr, 0, ws + at.y, x_dtype};
+    g2.E = E;
+    g2.R = R;
+    g2.offsets = offsets;
+    rc = mx4_grouped_validate(g2);
+    if (rc) return rc;
+    const CombineArgs ca{ws + at.y, x_dtype, R, T, K, top_k, pos, weights, out};
+    rc = device_check();
+    if (rc) return rc;
+    hipStream_t st = (hipStream_t)stream;
+    hipError_t e = launch_route(ra, st);
+    if (e != hipSuccess) return hip_fail(e, "routing launch");
+    e = launch_mx4_quantize(qa, st);
+    if (e != hipSuccess) return hip_fail(e, "mx4 quantizer launch");
+    e = launch_mx4_gemm(g1, st);
+    if (e != hipSuccess) return hip_fail(e, "mx4 gated grouped gemm launch");
+    e = launch_mx4_gemm(g2, st);
+    if (e != hipSuccess) return hip_fail(e, "mx4 grouped gemm launch");
+    e = launch_combine(ca, st);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "combining launch");
 }
 
 int w4a4_linear_noalloc(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,

@@ -1,0 +1,257 @@
+// MX4 quantiser (optional Hadamard rotation, block scales, e2m1 codes) and its
+// inverse.
+//
+// Mathematics.  Per row and group of g (if rotated), in fp32:
+//   y = H_g (x . sign_in) * fp32(1 / sqrt(g)) . sign_out,
+// the fast Walsh-Hadamard transform with butterflies of distance 1, 2, 4, ...
+// in that order (the order fixes every rounding, so the result is defined to
+// the bit).  Per 32 consecutive y: X = max(floor(log2(absmax)) - 2, -127),
+// codes = e2m1(y / 2^X) to nearest, ties to the even code, saturated at 6.  y
+// stays in fp32 until the codes are taken: there is no rounding in between.
+// A block that holds a NaN or an infinity gets scale byte 255 and codes 0.
+#include "common.hpp"
+#include "mx4.hpp"
+
+namespace w4a4 {
+
+namespace {
+
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mq_rsrc(const void* base, uint64_t bytes)
+{
+    const uint32_t n = bytes > 0xffffffffull ? 0xffffffffu : (uint32_t)bytes;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)n, 0x00020000);
+}
+
+// the value of the lane whose index differs in bit D (D = 1, 2, 4, 8, 16)
+template <int D> __device__ __forceinline__ uint32_t mq_xor(uint32_t v)
+{
+    if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);        // quad [1,0,3,2]
+    else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true);   // quad [2,3,0,1]
+    else if constexpr (D == 4)                                                             // 7 - i, then quad [3,2,1,0]
+        return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
+    else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, 0xf, 0xf, true);  // row rotate by 8
+    else return __builtin_amdgcn_ds_swizzle(v, 0x401f);                                    // xor 16
+}
+
+template <int D> __device__ __forceinline__ void butterfly_across(float (&v)[8], int lane)
+{
+    const float s = (lane & D) ? -1.0f : 1.0f;   // upper partner: other - own, lower: own + other
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = __builtin_fmaf(s, v[e], __uint_as_float(mq_xor<D>(__float_as_uint(v[e]))));
+}
+
+template <int G> __device__ __forceinline__ void rotate8(float (&v)[8], int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (!(e & d)) {
+                const float a = v[e], b = v[e + d];
+                v[e] = add_rn(a, b);
+                v[e + d] = add_rn(a, -b);
+            }
+    if constexpr (G >= 16) butterfly_across<1>(v, lane);
+    if constexpr (G >= 32) butterfly_across<2>(v, lane);
+    if constexpr (G >= 64) butterfly_across<4>(v, lane);
+    if constexpr (G >= 128) butterfly_across<8>(v, lane);
+    if constexpr (G >= 256) butterfly_across<16>(v, lane);
+}
+
+template <int G> constexpr float inv_sqrt()
+{
+    // fp32(1 / sqrt(g))
+    return G == 16 ? 0.25f : G == 32 ? 0.17677669529663687f : G == 64 ? 0.125f : G == 128 ? 0.08838834764831845f : 0.0625f;
+}
+
+// one byte of signs per element -> sign bits
+__device__ __forceinline__ uint32_t sign_of(const v2u s, int e)
+{
+    return (e < 4 ? s[0] << (24 - 8 * e) : s[1] << (24 - 8 * (e - 4))) & 0x80000000u;
+}
+
+// A half wave holds 256 consecutive k of a row, eight per lane; a workgroup
+// takes U * 8 rows of one slab, so its scale bytes lie side by side, and every
+// lane has U rows in flight.  VEC: 16-byte loads from contiguous aligned rows;
+// else one load per element at any strides.
+template <int DT, int G, bool VEC, int U>
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4QuantArgs a)
+{
+    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31;
+    const int64_t M = a.M, K = a.K;
+    const int64_t slab = blockIdx.y;
+    const int64_t k0 = slab * kMxSlab + l32 * 8;
+    const int64_t row0 = (int64_t)blockIdx.x * (8 * U) + (tid >> 5);
+    const bool in_k = k0 < K;
+    v2u si = {0, 0}, so = {0, 0};
+    if constexpr (G > 0) {
+        const int o = (l32 * 8) & (G - 1);
+        if (a.sign_in) si = (v2u){((const unsigned*)(a.sign_in + o))[0], ((const unsigned*)(a.sign_in + o))[1]};
+        if (a.sign_out) so = (v2u){((const unsigned*)(a.sign_out + o))[0], ((const unsigned*)(a.sign_out + o))[1]};
+    }
+    constexpr int ESZ = DT == F32 ? 4 : 2;
+    uint32_t raw[U][2 * ESZ];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + 8 * u;
+        const bool in = in_k && row < M;
+#pragma unroll
+        for (int i = 0; i < 2 * ESZ; ++i) raw[u][i] = 0;
+        if constexpr (VEC) {
+            if (in) {
+                const v4u* p = (const v4u*)((const char*)a.x + (row * a.sm + k0) * ESZ);
+#pragma unroll
+                for (int i = 0; i < ESZ / 2; ++i) {
+                    const v4u t = p[i];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) raw[u][4 * i + c] = t[c];
+                }
+            }
+        } else if (in) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t at = row * a.sm + (k0 + e) * a.sk;
+                if constexpr (DT == F32) raw[u][e] = ((const uint32_t*)a.x)[at];
+                else raw[u][e >> 1] |= (uint32_t)((const uint16_t*)a.x)[at] << (16 * (e & 1));
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + 8 * u;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (DT == F32) v[e] = __uint_as_float(raw[u][e]);
+            else v[e] = h_to_f32<DT>((uint16_t)(raw[u][e >> 1] >> (16 * (e & 1))));
+        }
+        if constexpr (G > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ sign_of(si, e));
+            rotate8<G>(v, lane);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __uint_as_float(__float_as_uint(mul_rn(v[e], inv_sqrt<G>())) ^ sign_of(so, e));
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+        m = max(m, mq_xor<1>(m));
+        m = max(m, mq_xor<2>(m));
+        const uint32_t ex = m >> 23;
+        const bool bad = ex == 255;
+        const uint32_t byte = bad ? 255u : ex > 2 ? ex - 2 : 0u;
+        const float sc = __uint_as_float(byte << 23);   // the conversion reads the exponent field only
+        uint32_t c = 0;
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], sc, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], sc, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], sc, 3);
+        if (bad) c = 0;
+        if (row < M) {
+            if (in_k) *(uint32_t*)(a.codes + row * (K >> 1) + (k0 >> 1)) = c;
+            if (!(lane & 3)) a.scales[(slab * M + row) * 8 + (l32 >> 2)] = (uint8_t)(in_k ? byte : 0u);
+        }
+    }
+}
+
+// Eight values per thread: 4 bytes of codes in, 16 or 32 bytes out.  The
+// fp32 products are exact; 16-bit outputs round once.
+template <int ODT>
+__global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, int64_t M, int64_t K,
+                                                             int64_t pieces, void* __restrict__ out)
+{
+    const int64_t per_row = K >> 3;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row, p = i - row * per_row;
+        const uint32_t c = ((const uint32_t*)codes)[i];
+        const int64_t blk = p >> 2;
+        const uint32_t byte = scales[((blk >> 3) * M + row) * 8 + (blk & 7)];
+        // 2^-127 is the subnormal 0x00400000; 255 is NaN
+        const float s = __uint_as_float(byte == 255 ? 0x7fc00000u : byte ? byte << 23 : 0x00400000u);
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        float v[8];
+        const f2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+        const f2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+        v[0] = mul_rn(v0[0], s); v[1] = mul_rn(v0[1], s); v[2] = mul_rn(v1[0], s); v[3] = mul_rn(v1[1], s);
+        v[4] = mul_rn(v2[0], s); v[5] = mul_rn(v2[1], s); v[6] = mul_rn(v3[0], s); v[7] = mul_rn(v3[1], s);
+        if constexpr (ODT == F32) {
+            v4u* o = (v4u*)out + 2 * i;
+            o[0] = (v4u){__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+            o[1] = (v4u){__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+        } else {
+            v4u o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = f32_to_h<ODT>(v[2 * e]) | ((uint32_t)f32_to_h<ODT>(v[2 * e + 1]) << 16);
+            ((v4u*)out)[i] = o;
+        }
+    }
+}
+
+template <int DT, int G, bool VEC> hipError_t quantize_u(const Mx4QuantArgs& a, hipStream_t st)
+{
+    // Four rows in flight per lane once that still leaves a workgroup for
+    // every CU several times over; a decode batch spreads over the CUs instead.
+    const unsigned slabs = (unsigned)mx4_slabs(a.K);
+    if ((a.M + 31) / 32 * slabs >= 1024)
+        hipLaunchKernelGGL((mx4_quantize_kernel<DT, G, VEC, 4>), dim3((unsigned)((a.M + 31) / 32), slabs), dim3(256), 0,
+                           st, a);
+    else
+        hipLaunchKernelGGL((mx4_quantize_kernel<DT, G, VEC, 1>), dim3((unsigned)((a.M + 7) / 8), slabs), dim3(256), 0,
+                           st, a);
+    return hipGetLastError();
+}
+
+template <int DT, int G> hipError_t quantize_g(const Mx4QuantArgs& a, hipStream_t st)
+{
+    const int esz = DT == F32 ? 4 : 2;
+    const bool vec = a.sk == 1 && (a.sm * esz) % 16 == 0 && (uintptr_t)a.x % 16 == 0;
+    return vec ? quantize_u<DT, G, true>(a, st) : quantize_u<DT, G, false>(a, st);
+}
+
+template <int DT> hipError_t quantize_dt(const Mx4QuantArgs& a, hipStream_t st)
+{
+    switch (a.g) {
+    case 0: return quantize_g<DT, 0>(a, st);
+    case 16: return quantize_g<DT, 16>(a, st);
+    case 32: return quantize_g<DT, 32>(a, st);
+    case 64: return quantize_g<DT, 64>(a, st);
+    case 128: return quantize_g<DT, 128>(a, st);
+    case 256: return quantize_g<DT, 256>(a, st);
+    }
+    return hipErrorNotSupported;
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, hipStream_t st)
+{
+    switch (a.dtype) {
+    case F32: return quantize_dt<F32>(a, st);
+    case F16: return quantize_dt<F16>(a, st);
+    case BF16: return quantize_dt<BF16>(a, st);
+    }
+    return hipErrorNotSupported;
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out,
+                                 int out_dtype, hipStream_t st)
+{
+    const int64_t pieces = M * (K >> 3);
+    const unsigned grid = (unsigned)((pieces + 255) / 256 < 65536 ? (pieces + 255) / 256 : 65536);
+    if (out_dtype == F32)
+        hipLaunchKernelGGL(mx4_dequantize_kernel<F32>, dim3(grid), dim3(256), 0, st, codes, scales, M, K, pieces, out);
+    else if (out_dtype == F16)
+        hipLaunchKernelGGL(mx4_dequantize_kernel<F16>, dim3(grid), dim3(256), 0, st, codes, scales, M, K, pieces, out);
+    else
+        hipLaunchKernelGGL(mx4_dequantize_kernel<BF16>, dim3(grid), dim3(256), 0, st, codes, scales, M, K, pieces, out);
+    return hipGetLastError();
+}
+
+}  // namespace w4a4

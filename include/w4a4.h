@@ -330,6 +330,97 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
                     size_t workspace_bytes, void* stream);
 
 /*
+ * MX4: microscaled 4-bit floating point, and products grouped by expert.
+ *   Format.  32 consecutive k of a row share a scale 2^X; elements are e2m1
+ *   codes (bit 3 the sign; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) that stand
+ *   for code * 2^X.  Quantising: X = floor(log2 absmax) - 2, at least -127;
+ *   codes to nearest, ties to the even code, saturated at 6.  Codes are
+ *   (rows, K/2) bytes, even k in the low nibble, 16-byte aligned.  Scale bytes
+ *   are X + 127 (255: the whole block is NaN, as where an activation block
+ *   holds a NaN or an infinity) in slabs of 256 k: byte b of row r in slab s,
+ *   at (s * rows + r) * 8 + b, scales k = 256 s + 32 b .. + 31; bytes past
+ *   K/32 are zero; 4-byte aligned.  w4a4_mx4_scales_size(rows, K) bytes.
+ *   K is a multiple of 32, at most 2^24; at most 2^28 rows.
+ *
+ * w4a4_quantize_mx4: rows of x (any strides; 16-byte aligned contiguous rows
+ *   take wide loads) to MX4.  g > 0 first rotates groups of g (a power of two
+ *   in [16, 256] dividing K) by diag(sign_in) . H_g . diag(sign_out) / sqrt(g)
+ *   in fp32, butterflies of distance 1, 2, 4, ... in that order, then one
+ *   multiplication by fp32(1 / sqrt(g)); the rotated values are not rounded
+ *   to x_dtype.  Signs as for w4a4_rotate_quant_hadamard.
+ * w4a4_dequantize_mx4: the values (M, K) in out_dtype, 16-byte aligned.
+ * w4a4_gemm_mx4: out[m][n] = O(sum_k a[m][k] w[n][k] + bias[n]), weights
+ *   (N, K) in MX4, fp32 sums on the scaled f8f6f4 matrix cores.
+ * w4a4_linear_mx4: quantiser and product back to back; bias in x_dtype; a
+ *   workspace of w4a4_linear_mx4_workspace_size(M, K) bytes, 16-byte aligned.
+ * w4a4_grouped_gemm_mx4: R sorted rows, expert e's being offsets[e] ..
+ *   offsets[e + 1] - 1 (device array of E + 1, not decreasing); sorted row i
+ *   is row rows[i] of the (M, K) codes (rows NULL: row i, and M = R) and meets
+ *   expert e's weights (E, N, K/2), scales (E, slabs, N, 8), bias (E, N).  An
+ *   index outside [0, M) counts as a zero row.  Rows from offsets[E] on are
+ *   written as zeros.
+ * w4a4_grouped_gated_mx4: the same product with N/2 gates followed by N/2 ups
+ *   (N % 64 == 0); the result is the MX4 form of silu(gate) * up, taken from
+ *   the fp32 sums: out_codes (R, N/4), out_scales (slabs of N/2, R, 8).
+ * w4a4_gemm_mx4_plan (host-only): the kernel these calls take for `rows` rows
+ *   (E = 0: dense): 0 skinny, 1 / 2 / 3 tiles of 64 / 128 / 256 rows, -1 none.
+ * w4a4_route_experts: per token (row of logits, `stride` elements apart) the
+ *   top_k experts by logit, equal logits by the lower index; NaN and -inf
+ *   logits are never taken, so a token can have fewer than top_k (expert -1,
+ *   weight 0, pos -1).  weights (T, top_k): softmax over the chosen
+ *   (renormalize != 0) or over all E.  The (token, choice) slots sorted by
+ *   expert, in slot order within one: offsets (E + 1), rows (T * top_k) the
+ *   token of each sorted row (-1 past the last), pos (T, top_k) the sorted row
+ *   of each slot.  E <= 1024, top_k <= 32.  A workspace of
+ *   w4a4_route_experts_workspace_size(T, E) bytes (0 for few tokens).
+ * w4a4_combine_experts: out[t] = sum_j weights[t][j] * y[pos[t][j]] in fp32, j
+ *   in order (pos -1 adds nothing), y (R, N) and out (T, N) in one dtype.
+ * w4a4_experts_mx4: route, quantise, gated product (w13: (E, 2 F, K), gates
+ *   first), product (w2: (E, K, F)), combine; the experts' rows are kept in
+ *   x_dtype between the last two.  Workspace of
+ *   w4a4_experts_mx4_workspace_size bytes, 16-byte aligned.
+ */
+size_t w4a4_mx4_scales_size(int64_t rows, int64_t K);
+int w4a4_quantize_mx4(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                      int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                      uint8_t* codes, uint8_t* scales, void* stream);
+int w4a4_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out,
+                        int out_dtype, void* stream);
+int w4a4_gemm_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
+                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const void* bias,
+                  int bias_dtype, void* out, int out_dtype, void* stream);
+int w4a4_gemm_mx4_plan(int64_t rows, int64_t K, int64_t N, int32_t E, int32_t gated, int* kernel);
+size_t w4a4_linear_mx4_workspace_size(int64_t M, int64_t K);
+int w4a4_linear_mx4(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                    int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const void* bias,
+                    void* out, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int w4a4_grouped_gemm_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
+                          const uint8_t* w_codes, const uint8_t* w_scales, int32_t E, int64_t N,
+                          const int32_t* offsets, const int32_t* rows, int64_t R, const void* bias,
+                          int bias_dtype, void* out, int out_dtype, void* stream);
+int w4a4_grouped_gated_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
+                           const uint8_t* w_codes, const uint8_t* w_scales, int32_t E, int64_t N,
+                           const int32_t* offsets, const int32_t* rows, int64_t R, const void* bias,
+                           int bias_dtype, uint8_t* out_codes, uint8_t* out_scales, void* stream);
+size_t w4a4_route_experts_workspace_size(int64_t T, int32_t E);
+int w4a4_route_experts(const void* logits, int dtype, int64_t T, int64_t stride, int32_t E,
+                       int32_t top_k, int32_t renormalize, float* weights, int32_t* experts,
+                       int32_t* rows, int32_t* pos, int32_t* offsets, void* workspace,
+                       size_t workspace_bytes, void* stream);
+int w4a4_combine_experts(const void* y, int dtype, int64_t R, int64_t N, const int32_t* pos,
+                         const float* weights, int64_t T, int32_t top_k, void* out, void* stream);
+size_t w4a4_experts_mx4_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k,
+                                       int x_dtype);
+int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m,
+                     int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                     const void* logits, int logits_dtype, int64_t logits_stride, int32_t E,
+                     int32_t top_k, int32_t renormalize, const uint8_t* w13_codes,
+                     const uint8_t* w13_scales, int64_t F, const uint8_t* w2_codes,
+                     const uint8_t* w2_scales, void* out, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
  * w4a4_linear for callers that cannot allocate device memory (code under
  * HIP graph capture, tight serving loops, harnesses that forbid hipMalloc):
  * the same arguments without the workspace, and the same kernels, which work
