@@ -1,14 +1,17 @@
 // The MX4 product out[m][n] = sum_k a[m][k] w[n][k] (+ bias[n]) on gfx950's
 // scaled f8f6f4 matrix cores, dense and grouped by expert.
 //
-// Mathematics.  v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 x 128 by
-// 128 x 16 e2m1 values, each run of 32 k of a row times its own power of two,
-// and adds to fp32.  Products of two e2m1 values are multiples of 1/4 up to
-// 36, so the sum over a block is exact; sums over blocks and steps are fp32.
-// Lane (j, q) (j = lane & 15, q = lane >> 4) supplies row j, one block of 32 k
-// and that block's scale byte.  Which 32 k lane group q holds is free as long
-// as both operands agree: here a step of 256 k gives group q the blocks 2q and
-// 2q + 1, two MFMAs (t = 0, 1) whose scales are bytes t of one 16-bit word.
+// Mathematics.  v_mfma_scale_f32_32x32x64_f8f6f4 (16x16x128) multiplies 32 x 64
+// by 64 x 32 (16 x 128 by 128 x 16) e2m1 values, each run of 32 k of a row
+// times its own power of two, and adds to fp32.  Products of two e2m1 values
+// are multiples of 1/4 up to 36, so the sum over a block is exact; sums over
+// blocks and steps are fp32.  A lane supplies one row, one block of 32 k and
+// that block's scale byte; which block is free as long as both operands agree.
+// A step is 256 k, the eight blocks of a scale slab: with 32 x 32 tiles lane
+// half h takes the blocks 4h .. 4h + 3, four MFMAs (t = 0 .. 3) whose scales
+// are the bytes of one word; with 16 x 16 tiles lane group q takes 2q, 2q + 1.
+// The tile kernel uses 32 x 32: one wave per SIMD reaches 8.1 PFLOP/s with it
+// and 4.9 with 16 x 16 (registers only, no memory).
 #include "common.hpp"
 #include "mx4.hpp"
 
@@ -44,6 +47,53 @@ template <int SB, int SA> __device__ __forceinline__ v4f mx_mfma(v4i w, v4i a, v
     const v8i w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, SB, (int)sw, SA, (int)sa);
 }
+
+// Four 32 x 32 MFMAs that share an activation fragment, byte T of every scale
+// word.  The accumulators are read and written in place in accumulation
+// registers (256 of them is all there are: any other allocation moves them
+// around), and the group stays where it is written: the compiler neither moves
+// it across barriers nor sees the matrix core's latencies.  s_nop 1: the two
+// wait states between a vector instruction's result and an MFMA that reads it.
+typedef float v16f __attribute__((ext_vector_type(16)));
+template <int T>
+__device__ __forceinline__ void mx_group(v16f (&c)[4], const v4i (&w)[4], const v4i& a, const uint32_t (&sw)[4], uint32_t sa)
+{
+#define MX_LINE(c, w, s, sel) \
+    "v_mfma_scale_f32_32x32x64_f8f6f4 " c ", " w ", %8, " c ", " s ", %13 " sel " cbsz:4 blgp:4\n\t"
+#define MX_FOUR(sel)                                                                                        \
+    asm volatile("s_nop 1\n\t" MX_LINE("%0", "%4", "%9", sel) MX_LINE("%1", "%5", "%10", sel)               \
+                     MX_LINE("%2", "%6", "%11", sel) MX_LINE("%3", "%7", "%12", sel)                        \
+                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                           \
+                 : "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]), "v"(a), "v"(sw[0]), "v"(sw[1]), "v"(sw[2]),  \
+                   "v"(sw[3]), "v"(sa))
+    if constexpr (T == 0) MX_FOUR("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+    if constexpr (T == 1) MX_FOUR("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+    if constexpr (T == 2) MX_FOUR("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+    if constexpr (T == 3) MX_FOUR("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef MX_FOUR
+#undef MX_LINE
+}
+// Accumulators that start at zero: an MFMA of zeros, in a quarter of the time
+// of sixteen register writes each.
+__device__ __forceinline__ void mx_clear(v16f (&c)[4])
+{
+    const v4i z = {0, 0, 0, 0};
+#define MX_ZERO(c) "v_mfma_f32_32x32x64_f8f6f4 " c ", %4, %4, 0 cbsz:4 blgp:4\n\t"
+    asm volatile("s_nop 1\n\t" MX_ZERO("%0") MX_ZERO("%1") MX_ZERO("%2") MX_ZERO("%3")
+                 : "=a"(c[0]), "=a"(c[1]), "=a"(c[2]), "=a"(c[3])
+                 : "v"(z));
+#undef MX_ZERO
+}
+// Before accumulators of mx_group are read by anything but another mx_group:
+// the wait states of the last MFMA.
+__device__ __forceinline__ void mx_settle(v16f (&c)[4])
+{
+    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
+}
+
+// An accumulator leaves its accumulation registers no earlier than here (the
+// compiler would copy all of them out ahead of the epilogue's branches).
+__device__ __forceinline__ void mx_here(v16f& c) { asm volatile("" : "+a"(c)); }
 
 // ---- which rows a workgroup takes --------------------------------------------
 struct MxRows {
@@ -137,34 +187,82 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t m)
     return ex == 255 ? 255u : ex > 2 ? ex - 2 : 0u;
 }
 
-__device__ __forceinline__ uint32_t mx_pack2(int odt, float lo, float hi)
+template <int ODT> __device__ __forceinline__ uint32_t mx_pack2(float lo, float hi)
 {
-    return odt == BF16 ? (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16)
-                       : (uint32_t)f32_to_f16(lo) | ((uint32_t)f32_to_f16(hi) << 16);
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    if constexpr (ODT == BF16) {
+        typedef __bf16 h2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){lo, hi}, h2));
+    } else {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){lo, hi}, h2));
+    }
 }
 
-// Sixteen consecutive outputs of one row, from column c on (those below N).
-// vec: rows are 16-byte aligned, so a 16-byte piece is all in or all out.
-__device__ __forceinline__ void mx_store16(const Mx4GemmArgs& a, int64_t row, int64_t c, bool vec, const float (&v)[16])
+// Whether a tile's outputs go out as 16-byte pieces: rows 16-byte aligned (a
+// piece is then all in or all out) and a tile's rows within 2^31 bytes.
+__device__ __forceinline__ bool mx_wide_stores(const Mx4GemmArgs& a)
 {
     const int esz = a.out_dtype == F32 ? 4 : 2;
-    char* o = (char*)a.out + (row * a.N + c) * esz;
-    if (!vec) {
+    return (a.N * esz) % 16 == 0 && (uintptr_t)a.out % 16 == 0 && a.N * esz < ((int64_t)1 << 23);
+}
+
+// The epilogue of a wave: rows row0 + 32 mt of the tile, sixteen consecutive
+// columns from n0 + c0 + 32 nt in this lane.  Wide stores are range-checked buffer stores, so that every wave issues the same
+// number of them, 4 MT times two (fp32: four), whatever the tile holds.
+template <int ODT, int MT>
+__device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
+                                            int64_t n0, int c0, int e, bool wide)
+{
+    constexpr int ESZ = ODT == F32 ? 4 : 2;
+    const int64_t N = a.N;
+    const __amdgpu_buffer_rsrc_t ro =
+        mx_rsrc((char*)a.out + (m0 * N + n0) * ESZ, ((int64_t)rows * N - n0) * ESZ);
+    const uint32_t rstep = (uint32_t)(32 * N * ESZ);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c + i < a.N) store_any(a.out_dtype, o, i, v[i]);
-    } else if (a.out_dtype == F32) {
+    for (int nt = 0; nt < 4; ++nt) {
+        const int64_t c = n0 + c0 + 32 * nt;
+        float bv[16];
+        if (a.bias) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            if (c + 4 * h < a.N) ((v4f*)o)[h] = (v4f){v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-    } else {
+            for (int i = 0; i < 16; ++i)
+                bv[i] = c + i < N ? load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + c + i) : 0.0f;
+        }
+        const uint32_t off = (uint32_t)((row0 * N + c0 + 32 * nt) * ESZ);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (c + 8 * h < a.N)
-                ((v4u*)o)[h] = (v4u){mx_pack2(a.out_dtype, v[8 * h], v[8 * h + 1]),
-                                     mx_pack2(a.out_dtype, v[8 * h + 2], v[8 * h + 3]),
-                                     mx_pack2(a.out_dtype, v[8 * h + 4], v[8 * h + 5]),
-                                     mx_pack2(a.out_dtype, v[8 * h + 6], v[8 * h + 7])};
+        for (int mt = 0; mt < MT; ++mt) {
+            float v[16];
+            mx_here(acc[mt][nt]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = acc[mt][nt][i];
+            if (a.bias) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = add_rn(v[i], bv[i]);
+            }
+            if (wide) {
+                if constexpr (ODT == F32) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            (v4u){__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]),
+                                  __float_as_uint(v[4 * p + 3])},
+                            ro, (int)(c + 4 * p < N ? off + mt * rstep + 16 * p : kOut), 0, 0);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            (v4u){mx_pack2<ODT>(v[8 * p], v[8 * p + 1]), mx_pack2<ODT>(v[8 * p + 2], v[8 * p + 3]),
+                                  mx_pack2<ODT>(v[8 * p + 4], v[8 * p + 5]), mx_pack2<ODT>(v[8 * p + 6], v[8 * p + 7])},
+                            ro, (int)(c + 8 * p < N ? off + mt * rstep + 16 * p : kOut), 0, 0);
+                }
+            } else if (row0 + 32 * mt < rows) {
+                char* o = (char*)a.out + ((m0 + row0 + 32 * mt) * N + c) * ESZ;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < N) store_any(ODT, o, i, v[i]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
+        }
     }
 }
 
@@ -173,26 +271,25 @@ __device__ __forceinline__ void mx_store16(const Mx4GemmArgs& a, int64_t row, in
 // steps of 256.
 //   * A step's codes (128 bytes a row) and scales (8 bytes a row) go global ->
 //     LDS by DMA into one of two slots.  16-byte chunk c of a row sits at
-//     c ^ swizzle(row), so that the sixteen lanes of every ds_read_b128 cycle
-//     (lanes j in {0-3, 12-15} of one 16-lane group and {4-11} of its
-//     neighbour) hit sixteen different 16-byte bank groups.
-//   * A step is two halves (t = 0, 1).  While half t's MFMAs run from
-//     registers, the fragments of the next half are read from LDS.  Between
-//     the halves the waves wait for the next step's DMA and meet; then nobody
+//     c ^ swizzle(row): a ds_read_b128 serves sixteen lanes a cycle (lanes
+//     {0-3, 12-15} of one group of sixteen and {4-11} of its neighbour), and
+//     these then hit sixteen different 16-byte bank groups.
+//   * A step is four quarters (t).  While quarter t's MFMAs run from registers,
+//     the fragments of the next one are read from LDS.  Before the last
+//     quarter the waves wait for the next step's DMA and meet: then nobody
 //     reads this step's slot any more, and the DMA of the step after the next
 //     goes out into it, a whole step ahead of its use.
-//   * The MFMA takes the weights as first operand, and the weight columns of
-//     four neighbouring column tiles are interleaved (tile nt, MFMA row c is
-//     column 16 (c >> 2) + 4 nt + (c & 3) of 64), so a lane ends with sixteen
-//     consecutive columns of one row.
+//   * The MFMA takes the weights as first operand, and MFMA row c of a column
+//     tile is column 16 ((c >> 2) & 1) + 4 (c >> 3) + (c & 3), so a lane ends
+//     with sixteen consecutive columns of one row.
 //   * Gated: a wave's 128 columns are 64 gates and the 64 ups that belong to
-//     them, so gate, up and the block of 32 results (two neighbouring lane
-//     groups) meet in registers: silu, product, block scale and codes are the
-//     epilogue, and the 2 x 16-bit intermediate is never written.
+//     them, so gate, up and the block of 32 results (two lane halves) meet in
+//     registers: silu, product, block scale and codes are the epilogue, and
+//     the 2 x 16-bit intermediate is never written.
 template <int BM, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int tiles_m, int tiles_n)
 {
-    constexpr int MT = BM / 32, NT = 8;
+    constexpr int MT = BM / 64, NT = 4;       // 32 x 32 tiles per wave
     constexpr int AB = BM * 128, BB = 256 * 128, SAB = BM * 8, SBB = 256 * 8;
     constexpr int SLOT = AB + BB + SAB + SBB;
     constexpr int AI = BM / 32;               // A DMA instructions per wave (8 rows each)
@@ -200,266 +297,331 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-    const int j = lane & 15, q = lane >> 4;
+    const int j = lane & 31, h = lane >> 5;
     const int wm = wave & 1, wn = wave >> 1;
     const int64_t K = a.K, N = a.N, pitch = K >> 1;
     const int nsteps = (int)((K + 255) / 256);
 
-    // ---- the tile
-    int64_t m0;
-    int rows, tn, e = 0;
+    const int kblocks = (int)(K >> 5);
+    const int64_t F = N >> 1;   // gated: number of results
+
+    // ---- tiles: this workgroup takes number blockIdx.x, + gridDim.x, ...
+    struct Tile {
+        int64_t m0;
+        int rows, tn, e;   // rows 0: none
+    };
+    int64_t ntiles;
     if constexpr (GROUPED) {
         MxRows r;
-        const int64_t total = mx_find<BM, false>(a, 0, 1, r) * tiles_n;
-        const int64_t t = blockIdx.x;
-        if (t >= total) {
-            mx_zero_rows(a, t - total, gridDim.x - total);
-            return;
-        }
-        // each XCD (workgroup index modulo 8) takes a contiguous range
-        const int64_t q8 = total >> 3, r8 = total & 7, xcd = t & 7;
-        const int64_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (t >> 3);
-        mx_find<BM, true>(a, tile, tiles_n, r);
-        // within an expert: groups of eight row tiles, row tiles fastest
-        const int in_e = (int)(tile - r.before * tiles_n);
-        const int per = 8 * tiles_n, grp = in_e / per, gm = min(r.cm - grp * 8, 8), in_g = in_e - grp * per;
-        const int m = grp * 8 + in_g % gm;
-        tn = in_g / gm;
-        e = r.e;
-        m0 = r.m0 + (int64_t)m * BM;
-        rows = min(r.rows - m * BM, BM);
+        ntiles = mx_find<BM, false>(a, 0, 1, r) * tiles_n;
+        mx_zero_rows(a, blockIdx.x, gridDim.x);
     } else {
-        const int total = tiles_m * tiles_n, t = blockIdx.x;
-        const int q8 = total >> 3, r8 = total & 7, xcd = t & 7;
-        const int tile = xcd * q8 + min(xcd, r8) + (t >> 3);
-        // groups of four row tiles: an XCD's 32 concurrent tiles span 4 x 8 blocks
-        const int per = 4 * tiles_n, grp = tile / per, gm = min(tiles_m - grp * 4, 4), in_g = tile - grp * per;
-        m0 = (int64_t)(grp * 4 + in_g % gm) * BM;
-        tn = in_g / gm;
-        rows = (int)min(a.M - m0, (int64_t)BM);
+        ntiles = (int64_t)tiles_m * tiles_n;
     }
-    const int64_t F = N >> 1;   // gated: number of results
-    const uint8_t* wb = a.b + (int64_t)e * N * pitch;
-    const uint8_t* wsb = a.sb + (int64_t)e * nsteps * N * 8;
+    auto tile_of = [&](int64_t t) {
+        Tile r{0, 0, 0, 0};
+        if (t >= ntiles) return r;
+        // each XCD (workgroup index modulo 8; the grid is a multiple of 8 or
+        // the tiles are its first) takes a contiguous range
+        const int64_t q8 = ntiles >> 3, r8 = ntiles & 7, xcd = t & 7;
+        const int64_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (t >> 3);
+        if constexpr (GROUPED) {
+            MxRows x;
+            mx_find<BM, true>(a, tile, tiles_n, x);
+            // within an expert: groups of eight row tiles, row tiles fastest
+            const int in_e = (int)(tile - x.before * tiles_n);
+            const int per = 8 * tiles_n, grp = in_e / per, gm = min(x.cm - grp * 8, 8), in_g = in_e - grp * per;
+            const int m = grp * 8 + in_g % gm;
+            r.tn = in_g / gm;
+            r.e = x.e;
+            r.m0 = x.m0 + (int64_t)m * BM;
+            r.rows = min(x.rows - m * BM, BM);
+        } else {
+            // groups of four row tiles: an XCD's 32 concurrent tiles span 4 x 8 blocks
+            const int tl = (int)tile, per = 4 * tiles_n, grp = tl / per, gm = min(tiles_m - grp * 4, 4), in_g = tl - grp * per;
+            r.m0 = (int64_t)(grp * 4 + in_g % gm) * BM;
+            r.tn = in_g / gm;
+            r.rows = (int)min(a.M - r.m0, (int64_t)BM);
+        }
+        return r;
+    };
 
     // ---- DMA: wave w moves rows [w BM/4, (w + 1) BM/4) of A and 64 weight columns
     const int l8 = lane >> 3, c8 = lane & 7;
     const int ar0 = wave * (BM / 4);
-    const int ca = c8 ^ ((((l8 >> 1) & 1) << 2) | ((l8 >> 2) & 1));
-    const int cb0 = c8 ^ (((l8 >> 1) & 1) << 2);
+    // (bits 1 and 2 of the row; bit 3, for columns bit 4, is the instruction's)
+    const int cs = c8 ^ (l8 >> 1);
     const bool gather = GROUPED && a.rows != nullptr;
-    const uint8_t* abase = gather ? a.a : a.a + m0 * pitch;
-    const uint8_t* sabase = gather ? a.sa : a.sa + m0 * 8;
-    const int64_t arows = gather ? a.M : rows;      // rows behind the resource
-    const int64_t srows = a.M;                      // rows of a scale slab
-    // the source row of tile row i, or one past the resource
-    auto src_row = [&](int i) -> int64_t {
-        if (!gather) return i;
-        if (i >= rows) return -1;
-        const int64_t s = a.rows[m0 + i];
-        return s >= 0 && s < a.M ? s : -1;
-    };
-    uint32_t avo[AI], savo[2];
-#pragma unroll
-    for (int i = 0; i < AI; ++i) {
-        const int64_t s = src_row(ar0 + 8 * i + l8);
-        avo[i] = s < 0 ? kOut : (uint32_t)(s * pitch + ca * 16);
-    }
-    // scales: 32 rows per 64-lane instruction; BM / 32 instructions in all
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r0 = BM == 256 ? wave * 64 + i * 32 : wave * 32;
-        const int64_t s = src_row(r0 + (lane >> 1));
-        savo[i] = s < 0 || r0 >= BM ? kOut : (uint32_t)(s * 8 + (lane & 1) * 4);
-    }
-    const __amdgpu_buffer_rsrc_t ra = mx_rsrc(abase, arows * pitch);
-    // the wave's 64 weight columns (gated: even waves gates, odd waves ups)
-    const int64_t col0 = GATED ? (int64_t)tn * 128 + (wave >> 1) * 64 : (int64_t)tn * 256 + wave * 64;
-    const int64_t ncols = GATED ? F : N, wcol = GATED ? (wave & 1) * F + col0 : col0;
-    const int64_t left = ncols - col0 < 0 ? 0 : ncols - col0 > 64 ? 64 : ncols - col0;
-    const __amdgpu_buffer_rsrc_t rb = mx_rsrc(wb + (left ? wcol : 0) * pitch, left * pitch);
+    const int64_t srows = a.M;               // rows of a scale slab
     const uint32_t bvo = (uint32_t)(l8 * pitch), bstep = (uint32_t)(8 * pitch);
-    const uint8_t* sbcol = wsb + (left ? wcol : 0) * 8;
-    const int kblocks = (int)(K >> 5);
-
-    auto issue = [&](int s) {
-        uint8_t* sl = smem + (s & 1) * SLOT;
-        const int ko = s * 128;
-        // chunks past K read zeros (offset past the resource)
-        const uint32_t ta = s * 8 + ca < kblocks ? 0u : kOut;
-        const uint32_t tb0 = (s * 8 + cb0 < kblocks ? cb0 * 16u : kOut) + bvo;
-        const uint32_t tb1 = (s * 8 + (cb0 ^ 1) < kblocks ? (cb0 ^ 1) * 16u : kOut) + bvo;
+    // of the tile whose steps are being moved:
+    uint32_t avo[AI], savo[2];               // lane offsets of rows and of their scales
+    __amdgpu_buffer_rsrc_t ra, rb;           // codes; empty where there is no tile
+    const uint8_t *sabase, *sbcol;           // scales
+    int64_t sabytes, sbbytes;
+    auto set_dma = [&](const Tile& t) {
+        // the source row of tile row i, or one past the resource
+        auto src_row = [&](int i) -> int64_t {
+            if (!gather) return i;
+            if (i >= t.rows) return -1;
+            const int64_t s = a.rows[t.m0 + i];
+            return s >= 0 && s < a.M ? s : -1;
+        };
 #pragma unroll
-        for (int i = 0; i < AI; ++i)
-            mx_dma<16>(ra, sl + (ar0 + 8 * i) * 128, avo[i] | ta, ko);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            mx_dma<16>(rb, sl + AB + (wave * 64 + 8 * i) * 128, ((i >> 2) ? tb1 : tb0) + i * bstep, ko);
-        const __amdgpu_buffer_rsrc_t rsa = mx_rsrc(sabase + s * srows * 8, arows * 8);
-        const __amdgpu_buffer_rsrc_t rsb = mx_rsrc(sbcol + s * N * 8, left * 8);
-        if constexpr (BM == 256) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                mx_dma<4>(rsa, sl + AB + BB + (wave * 64 + i * 32) * 8, savo[i], 0);
-        } else if (wave * 32 < BM) {
-            mx_dma<4>(rsa, sl + AB + BB + wave * 32 * 8, savo[0], 0);
+        for (int i = 0; i < AI; ++i) {
+            const int64_t s = src_row(ar0 + 8 * i + l8);
+            avo[i] = s < 0 ? kOut : (uint32_t)(s * pitch);
         }
+        // scales: 32 rows per 64-lane instruction; BM / 32 instructions in all
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            mx_dma<4>(rsb, sl + AB + BB + SAB + (wave * 64 + i * 32) * 8, lane * 4 + i * 256, 0);
+        for (int i = 0; i < 2; ++i) {
+            const int r0 = BM == 256 ? wave * 64 + i * 32 : wave * 32;
+            const int64_t s = src_row(r0 + (lane >> 1));
+            savo[i] = s < 0 || r0 >= BM ? kOut : (uint32_t)(s * 8 + (lane & 1) * 4);
+        }
+        const int64_t arows = t.rows == 0 ? 0 : gather ? a.M : t.rows;   // rows behind the resource
+        ra = mx_rsrc(gather ? a.a : a.a + t.m0 * pitch, arows * pitch);
+        sabase = gather ? a.sa : a.sa + t.m0 * 8;
+        sabytes = arows * 8;
+        // the wave's 64 weight columns (gated: even waves gates, odd waves ups)
+        const int64_t col0 = GATED ? (int64_t)t.tn * 128 + (wave >> 1) * 64 : (int64_t)t.tn * 256 + wave * 64;
+        const int64_t ncols = t.rows == 0 ? 0 : GATED ? F : N;
+        const int64_t left = ncols - col0 < 0 ? 0 : ncols - col0 > 64 ? 64 : ncols - col0;
+        const int64_t wcol = left == 0 ? 0 : GATED ? (wave & 1) * F + col0 : col0;
+        rb = mx_rsrc(a.b + ((int64_t)t.e * N + wcol) * pitch, left * pitch);
+        sbcol = a.sb + ((int64_t)t.e * nsteps * N + wcol) * 8;
+        sbbytes = left * 8;
     };
 
-    // ---- fragments
-    const int arow = wm * (BM / 2) + j, asw = (((j >> 1) & 1) << 2) | ((j >> 2) & 1);
-    const int bcol = wn * 128 + 16 * (j >> 2) + (j & 3), bsw = (((j >> 1) & 1) << 2) | ((j >> 3) & 1);
-    const int ao = arow * 128, bo = AB + bcol * 128;
-    const int ac = ((2 * q) ^ asw) * 16, bc = ((2 * q) ^ bsw) * 16;
-    const int so_a = AB + BB + arow * 8 + 2 * q, so_b = AB + BB + SAB + bcol * 8 + 2 * q;
-    v4i fa[2][MT], fb[2][NT];
-    uint32_t fsa[MT], fsb[NT];
-    v4f acc[MT][NT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = (v4f){0.f, 0.f, 0.f, 0.f};
-    auto read = [&](int slot, int t, v4i (&xa)[MT], v4i (&xb)[NT]) {
-        const uint8_t* sl = smem + slot * SLOT;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            xb[nt] = *(const v4i*)(sl + bo + ((nt >> 2) * 64 + (nt & 3) * 4) * 128 + (bc ^ (t * 16)));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) xa[mt] = *(const v4i*)(sl + ao + mt * 16 * 128 + (ac ^ (t * 16)));
+    // The DMA of one step, an instruction at a time: `Dma` holds what its
+    // instructions share.
+    constexpr int SAI = BM == 256 ? 2 : 1, DMAS = AI + 8 + SAI + 2;
+    struct Dma {
+        uint8_t* sl;
+        int ko;
+        uint32_t t0, t1;   // chunk cs and its partner cs ^ 4
+        __amdgpu_buffer_rsrc_t rsa, rsb;
     };
-    auto read_scales = [&](int slot, uint32_t (&xa)[MT], uint32_t (&xb)[NT]) {
-        const uint8_t* sl = smem + slot * SLOT;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            xb[nt] = *(const uint16_t*)(sl + so_b + ((nt >> 2) * 64 + (nt & 3) * 4) * 8);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) xa[mt] = *(const uint16_t*)(sl + so_a + mt * 16 * 8);
+    auto dma_of = [&](int slot, int s) {
+        // chunks past K read zeros (offset past the resource)
+        return Dma{smem + slot * SLOT, s * 128, s * 8 + cs < kblocks ? cs * 16u : kOut,
+                   s * 8 + (cs ^ 4) < kblocks ? (cs ^ 4) * 16u : kOut, mx_rsrc(sabase + s * srows * 8, sabytes),
+                   mx_rsrc(sbcol + s * N * 8, sbbytes)};
     };
+    auto dma = [&](const Dma& d, int n) {
+        if (n < AI) {
+            // (a row offset or a chunk past the resource stays past it: both
+            // are below 2^31 otherwise)
+            const uint32_t c = (n & 1) ? d.t1 : d.t0, r = avo[n < AI ? n : 0];
+            mx_dma<16>(ra, d.sl + (ar0 + 8 * n) * 128, (r + (c & ~kOut)) | ((r | c) & kOut), d.ko);
+        } else if (n < AI + 8) {
+            const int i = n - AI;
+            mx_dma<16>(rb, d.sl + AB + (wave * 64 + 8 * i) * 128, ((i & 2) ? d.t1 : d.t0) + bvo + i * bstep, d.ko);
+        } else if (n < AI + 8 + SAI) {
+            const int i = n - AI - 8;
+            if constexpr (BM == 256)
+                mx_dma<4>(d.rsa, d.sl + AB + BB + (wave * 64 + i * 32) * 8, savo[i & 1], 0);
+            else if (wave * 32 < BM)
+                mx_dma<4>(d.rsa, d.sl + AB + BB + wave * 32 * 8, savo[0], 0);
+        } else {
+            const int i = n - AI - 8 - SAI;
+            mx_dma<4>(d.rsb, d.sl + AB + BB + SAB + (wave * 64 + i * 32) * 8, lane * 4 + i * 256, 0);
+        }
+    };
+    // The steps of all tiles form one sequence; the DMA runs up to two steps,
+    // so up to two tiles, ahead of the MFMAs.
+    Tile cur = tile_of(blockIdx.x), q1{0, 0, 0, 0}, q2{0, 0, 0, 0};
+    if (cur.rows == 0) return;
+    int64_t t_dma = blockIdx.x;
+    int s_dma = 0, ahead = 0;
+    set_dma(cur);
+    auto advance = [&]() {
+        if (++s_dma < nsteps) return;
+        s_dma = 0;
+        t_dma += gridDim.x;
+        const Tile t = tile_of(t_dma);
+        set_dma(t);
+        (ahead == 0 ? q1 : q2) = t;
+        ++ahead;
+    };
+    auto issue = [&](int slot) {
+        const Dma d = dma_of(slot, s_dma);
+#pragma unroll
+        for (int n = 0; n < DMAS; ++n) dma(d, n);
+    };
+
+    // ---- fragments: row tile mt is rows arow + 32 mt, column tile nt columns
+    // bcol + 32 nt, chunk 4h + t
+    const int arow = wm * (BM / 2) + j, asw = (j >> 1) & 7;
+    const int bc_ = 16 * ((j >> 2) & 1) + 4 * (j >> 3) + (j & 3), bcol = wn * 128 + bc_;
+    const int bsw = ((bc_ >> 1) & 3) | (((bc_ >> 4) & 1) << 2);
+    const int ao = arow * 128 + ((4 * h) ^ asw) * 16, bo = AB + bcol * 128 + ((4 * h) ^ bsw) * 16;
+    const int so_a = AB + BB + arow * 8 + 4 * h, so_b = AB + BB + SAB + bcol * 8 + 4 * h;
+    v4i fa[2][MT], fb[2][NT];            // fragments of two quarters
+    uint32_t fsa[MT], fsb[NT], nsa[MT], nsb[NT];   // scale words of this step and the next
+    // fragment i of quarter t, in the order of first use; scale word i of a step
+    auto read = [&](int sl, int t, int i) {
+        if (i < NT) fb[t & 1][i] = *(const v4i*)(smem + ((sl + bo) ^ (t * 16)) + i * 32 * 128);
+        else fa[t & 1][i - NT] = *(const v4i*)(smem + ((sl + ao) ^ (t * 16)) + (i - NT) * 32 * 128);
+    };
+    auto read_scale = [&](int sl, int i) {
+        if (i < NT) nsb[i] = *(const uint32_t*)(smem + sl + so_b + i * 32 * 8);
+        else nsa[i - NT] = *(const uint32_t*)(smem + sl + so_a + (i - NT) * 32 * 8);
+    };
+    constexpr int FR = MT + NT;
 
     issue(0);
     __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (nsteps > 1) issue(1);
-    read(0, 0, fa[0], fb[0]);
-    read_scales(0, fsa, fsb);
-
-    for (int s = 0; s < nsteps; ++s) {
-        // ---- half 0: read half 1 of this step
-        read(s & 1, 1, fa[1], fb[1]);
+    advance();
+    issue(1);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                acc[mt][nt] = mx_mfma<0, 0>(fb[0][nt], fa[0][mt], acc[mt][nt], fsb[nt], fsa[mt]);
-#pragma unroll
-        for (int i = 0; i < MT + NT; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, MT * NT / (MT + NT), 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0): the next step has landed, this one is read
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        // ---- half 1: DMA of the step after the next, read half 0 of the next
-        // (past the last step: of a slot that holds an older step, unused)
-        if (s + 2 < nsteps) issue(s + 2);
-        uint32_t nsa[MT], nsb[NT];
-        read((s & 1) ^ 1, 0, fa[0], fb[0]);
-        read_scales((s & 1) ^ 1, nsa, nsb);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                acc[mt][nt] = mx_mfma<1, 1>(fb[1][nt], fa[1][mt], acc[mt][nt], fsb[nt], fsa[mt]);
-#pragma unroll
-        for (int i = 0; i < MT + NT; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, MT * NT / (MT + NT), 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) fsb[nt] = nsb[nt];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) fsa[mt] = nsa[mt];
+    for (int i = 0; i < FR; ++i) {
+        read(0, 0, i);
+        read_scale(0, i);
     }
+    // A quarter: MT groups of four MFMAs; behind each, its share of the next
+    // quarter's fragment reads, and in the last quarter of the next step's
+    // scale words and of the DMA, under the MFMAs' time
+    const int row0 = wm * (BM / 2) + j;    // this lane's row (+ 32 mt), and of the
+    const int c0 = wn * 128 + 16 * h;      // columns sixteen from c0 + 32 nt
+    const bool wide = !GATED && mx_wide_stores(a);
+    int slot = 0, stores = 0;              // stores: the last epilogue's, if they may stay in flight
+    for (;;) {
+        v16f acc[MT][NT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) mx_clear(acc[mt]);
+        for (int s = 0; s < nsteps; ++s) {
+            const int cur_s = slot * SLOT, nxt_s = SLOT - cur_s;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) fsb[i] = nsb[i];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) fsa[i] = nsa[i];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                mx_group<0>(acc[mt], fb[0], fa[0][mt], fsb, fsa[mt]);
+#pragma unroll
+                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) read(cur_s, 1, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                mx_group<1>(acc[mt], fb[1], fa[1][mt], fsb, fsa[mt]);
+#pragma unroll
+                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) read(cur_s, 2, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                mx_group<2>(acc[mt], fb[0], fa[0][mt], fsb, fsa[mt]);
+#pragma unroll
+                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) read(cur_s, 3, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // The next step has landed, this one is read.  Its DMA went out before
+            // the previous tile's stores, which may stay in flight in a tile's
+            // first step.
+            asm volatile("s_waitcnt lgkmcnt(0)\n\t"
+                         "s_cmp_eq_u32 %0, 0\n\t"
+                         "s_cbranch_scc1 1f\n\t"
+                         "s_waitcnt vmcnt(%1)\n\t"
+                         "s_branch 2f\n"
+                         "1:\n\t"
+                         "s_waitcnt vmcnt(0)\n"
+                         "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"(8 * MT) : "memory", "scc");
+            stores = 0;
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            advance();
+            const Dma d = dma_of(slot, s_dma);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                mx_group<3>(acc[mt], fb[1], fa[1][mt], fsb, fsa[mt]);
+#pragma unroll
+                for (int i = mt * DMAS / MT; i < (mt + 1) * DMAS / MT; ++i) dma(d, i);
+#pragma unroll
+                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) {
+                    read(nxt_s, 0, i);   // (past the last step: of an older one, unused)
+                    read_scale(nxt_s, i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            slot ^= 1;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) mx_settle(acc[mt]);
 
-    // ---- epilogue: lane (j, q) holds row wm BM/2 + 16 mt + j, and of each
-    // half u of the wave's 128 columns the sixteen from 16 q
-    if constexpr (GATED) {
-        const int64_t f0 = (int64_t)tn * 128 + wn * 64 + 16 * q;
-        const bool in_f = f0 < F;     // F is a multiple of 32, so are the blocks
+        // ---- epilogue
+        if constexpr (GATED) {
+            const int64_t R = GROUPED ? a.R : a.M;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int row = wm * (BM / 2) + 16 * mt + j;
-            float v[16];
-            uint32_t m = 0;
+            for (int nt = 0; nt < 2; ++nt) {
+                const int64_t f0 = (int64_t)cur.tn * 128 + wn * 64 + 32 * nt + 16 * h;
+                const bool in_f = f0 < F;     // F is a multiple of 32, so are the blocks
+                float bg[16], bu[16];
+                if (a.bias) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float g = acc[mt][i >> 2][i & 3], u = acc[mt][4 + (i >> 2)][i & 3];
-                if (a.bias && in_f) {
-                    g = add_rn(g, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + f0 + i));
-                    u = add_rn(u, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + F + f0 + i));
+                    for (int i = 0; i < 16; ++i) {
+                        bg[i] = in_f ? load_any_f32(a.bias_dtype, a.bias, (int64_t)cur.e * N + f0 + i) : 0.0f;
+                        bu[i] = in_f ? load_any_f32(a.bias_dtype, a.bias, (int64_t)cur.e * N + F + f0 + i) : 0.0f;
+                    }
                 }
-                v[i] = mx_gated(g, u);
-                m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-            }
-            m = max(m, (uint32_t)__builtin_amdgcn_ds_swizzle((int)m, 0x401f));   // the block's other sixteen
-            const uint32_t byte = mx_scale_byte(m);
-            const float sc = __uint_as_float(byte << 23);
-            uint32_t c[2] = {0, 0};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                c[h] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[h], v[8 * h + 0], v[8 * h + 1], sc, 0);
-                c[h] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[h], v[8 * h + 2], v[8 * h + 3], sc, 1);
-                c[h] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[h], v[8 * h + 4], v[8 * h + 5], sc, 2);
-                c[h] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[h], v[8 * h + 6], v[8 * h + 7], sc, 3);
-                if (byte == 255) c[h] = 0;
-            }
-            if (row < rows) {
-                const int64_t R = GROUPED ? a.R : a.M;
-                if (in_f) *(v2u*)(a.out_codes + ((m0 + row) * F + f0) / 2) = (v2u){c[0], c[1]};
-                // one lane per block writes its scale; columns past F, up to
-                // the end of the slab (which a last tile may fill only half),
-                // get zeros
-                if (!(q & 1)) {
-                    uint8_t* o = a.out_scales + ((f0 >> 8) * R + m0 + row) * 8 + ((f0 >> 5) & 7);
-                    o[0] = (uint8_t)(in_f ? byte : 0u);
-                    if (tn == tiles_n - 1 && !(tn & 1)) o[4] = 0;
+                for (int mt = 0; mt < MT; ++mt) {
+                    float v[16];
+                    uint32_t m = 0;
+                    mx_here(acc[mt][nt]);
+                    mx_here(acc[mt][2 + nt]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float g = acc[mt][nt][i], u = acc[mt][2 + nt][i];
+                        if (a.bias) {
+                            g = add_rn(g, bg[i]);
+                            u = add_rn(u, bu[i]);
+                        }
+                        v[i] = mx_gated(g, u);
+                        m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+                    }
+                    m = max(m, (uint32_t)__shfl_xor((int)m, 32));   // the block's other sixteen
+                    const uint32_t byte = mx_scale_byte(m);
+                    const float sc = __uint_as_float(byte << 23);
+                    uint32_t c[2] = {0, 0};
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 0], v[8 * p + 1], sc, 0);
+                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 2], v[8 * p + 3], sc, 1);
+                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 4], v[8 * p + 5], sc, 2);
+                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 6], v[8 * p + 7], sc, 3);
+                        if (byte == 255) c[p] = 0;
+                    }
+                    const int row = row0 + 32 * mt;
+                    if (row < cur.rows) {
+                        if (in_f) *(v2u*)(a.out_codes + ((cur.m0 + row) * F + f0) / 2) = (v2u){c[0], c[1]};
+                        // one lane per block writes its scale; columns past F, up
+                        // to the end of the slab (which a last tile may fill only
+                        // half), get zeros
+                        if (h == 0) {
+                            uint8_t* o = a.out_scales + ((f0 >> 8) * R + cur.m0 + row) * 8 + ((f0 >> 5) & 7);
+                            o[0] = (uint8_t)(in_f ? byte : 0u);
+                            if (cur.tn == tiles_n - 1 && !(cur.tn & 1)) o[4] = 0;
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);   // one row tile's values at a time
+        } else {
+            const int64_t n0 = (int64_t)cur.tn * 256;
+            if (a.out_dtype == BF16) mx_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
+            else if (a.out_dtype == F16) mx_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
+            else mx_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
+            stores = wide && !a.bias;   // (bias loads wait for what went before them)
         }
-    } else {
-        const int esz = a.out_dtype == F32 ? 4 : 2;
-        const bool vec = (N * esz) % 16 == 0 && (uintptr_t)a.out % 16 == 0;
-        // sixteen consecutive columns of one row: half u of the wave's 128
-        const int64_t c0 = (int64_t)tn * 256 + wn * 128 + 16 * q;
-        float bv[2][16];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int64_t c = c0 + 64 * (i >> 4) + (i & 15);
-            bv[i >> 4][i & 15] = a.bias && c < N ? load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + c) : 0.0f;
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int row = wm * (BM / 2) + 16 * mt + j;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = acc[mt][4 * u + (i >> 2)][i & 3];
-                    if (a.bias) v[i] = add_rn(v[i], bv[u][i]);
-                }
-                if (row < rows) mx_store16(a, m0 + row, c0 + 64 * u, vec, v);
-                __builtin_amdgcn_sched_barrier(0);   // one row tile's values at a time
-            }
-        }
+        cur = q1;
+        q1 = q2;
+        --ahead;
+        if (cur.rows == 0) break;
     }
 }
 
@@ -615,20 +777,22 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
     }
 }
 
+// One workgroup per CU (LDS holds one), which takes tiles in turn.
+constexpr int64_t kTileGrid = 256;
+
 template <int BM> hipError_t launch_tile(const Mx4GemmArgs& a, hipStream_t st)
 {
     const bool gated = a.out_codes != nullptr;
     const int64_t tn = gated ? (a.N / 2 + 127) / 128 : (a.N + 255) / 256;
-    if (a.E) {
-        const int64_t tm = a.R / BM + (a.E < a.R ? a.E : a.R) + 1;
-        if (gated)
-            hipLaunchKernelGGL((mx4_tile_kernel<BM, true, true>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, 0, (int)tn);
-        else
-            hipLaunchKernelGGL((mx4_tile_kernel<BM, true, false>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, 0, (int)tn);
-    } else {
-        const int64_t tm = (a.M + BM - 1) / BM;
-        hipLaunchKernelGGL((mx4_tile_kernel<BM, false, false>), dim3((unsigned)(tm * tn)), dim3(256), 0, st, a, (int)tm, (int)tn);
-    }
+    // (grouped: at most this many, the device knows)
+    const int64_t tm = a.E ? a.R / BM + (a.E < a.R ? a.E : a.R) : (a.M + BM - 1) / BM;
+    const unsigned grid = (unsigned)(tm * tn < kTileGrid ? tm * tn : kTileGrid);
+    if (!a.E)
+        hipLaunchKernelGGL((mx4_tile_kernel<BM, false, false>), dim3(grid), dim3(256), 0, st, a, (int)tm, (int)tn);
+    else if (gated)
+        hipLaunchKernelGGL((mx4_tile_kernel<BM, true, true>), dim3(grid), dim3(256), 0, st, a, 0, (int)tn);
+    else
+        hipLaunchKernelGGL((mx4_tile_kernel<BM, true, false>), dim3(grid), dim3(256), 0, st, a, 0, (int)tn);
     return hipGetLastError();
 }
 
