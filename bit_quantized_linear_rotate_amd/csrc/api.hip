@@ -183,6 +183,8 @@ int mx4_gemm_validate(const Mx4GemmArgs& a)
     if (a.N < 0) return fail(W4A4_INVALID, "negative size");
     rc = mx4_operand(a.b, a.sb, a.N, a.K, "weights");
     if (rc) return rc;
+    if (mx4_scales_bytes(a.M, a.K) > (size_t)1 << 31 || mx4_scales_bytes(a.N, a.K) > (size_t)1 << 31)
+        return fail(W4A4_UNSUPPORTED, "an operand with more than 2^31 bytes of scales");
     const bool gated = a.out_codes || a.out_scales;
     if ((!gated && !dtype_ok(a.out_dtype)) || (a.bias && !dtype_ok(a.bias_dtype)))
         return fail(W4A4_UNSUPPORTED, "unknown dtype code");

@@ -48,30 +48,25 @@ template <int SB, int SA> __device__ __forceinline__ v4f mx_mfma(v4i w, v4i a, v
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, SB, (int)sw, SA, (int)sa);
 }
 
-// Four 32 x 32 MFMAs that share an activation fragment, byte T of every scale
-// word.  The accumulators are read and written in place in accumulation
-// registers (256 of them is all there are: any other allocation moves them
-// around), and the group stays where it is written: the compiler neither moves
-// it across barriers nor sees the matrix core's latencies.  s_nop 1: the two
-// wait states between a vector instruction's result and an MFMA that reads it.
+// One 32 x 32 MFMA with byte T of its scale words.  The accumulators are read
+// and written in place in accumulation registers (256 of them is all there
+// are: any other allocation moves them around), and the instruction stays where
+// it is written: the compiler neither moves it across barriers nor sees the
+// matrix core's latencies.  s_nop 1: the two wait states between a vector
+// instruction's result and an MFMA that reads it (it passes under the MFMA
+// before).
 typedef float v16f __attribute__((ext_vector_type(16)));
-template <int T>
-__device__ __forceinline__ void mx_group(v16f (&c)[4], const v4i (&w)[4], const v4i& a, const uint32_t (&sw)[4], uint32_t sa)
+template <int T> __device__ __forceinline__ void mx_mma(v16f& c, const v4i& w, const v4i& a, uint32_t sw, uint32_t sa)
 {
-#define MX_LINE(c, w, s, sel) \
-    "v_mfma_scale_f32_32x32x64_f8f6f4 " c ", " w ", %8, " c ", " s ", %13 " sel " cbsz:4 blgp:4\n\t"
-#define MX_FOUR(sel)                                                                                        \
-    asm volatile("s_nop 1\n\t" MX_LINE("%0", "%4", "%9", sel) MX_LINE("%1", "%5", "%10", sel)               \
-                     MX_LINE("%2", "%6", "%11", sel) MX_LINE("%3", "%7", "%12", sel)                        \
-                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                           \
-                 : "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]), "v"(a), "v"(sw[0]), "v"(sw[1]), "v"(sw[2]),  \
-                   "v"(sw[3]), "v"(sa))
-    if constexpr (T == 0) MX_FOUR("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
-    if constexpr (T == 1) MX_FOUR("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
-    if constexpr (T == 2) MX_FOUR("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
-    if constexpr (T == 3) MX_FOUR("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
-#undef MX_FOUR
-#undef MX_LINE
+#define MX_MMA(sel)                                                                                           \
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 " sel " cbsz:4 blgp:4"   \
+                 : "+a"(c)                                                                                    \
+                 : "v"(w), "v"(a), "v"(sw), "v"(sa))
+    if constexpr (T == 0) MX_MMA("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+    if constexpr (T == 1) MX_MMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+    if constexpr (T == 2) MX_MMA("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+    if constexpr (T == 3) MX_MMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef MX_MMA
 }
 // Accumulators that start at zero: an MFMA of zeros, in a quarter of the time
 // of sixteen register writes each.
@@ -84,7 +79,7 @@ __device__ __forceinline__ void mx_clear(v16f (&c)[4])
                  : "v"(z));
 #undef MX_ZERO
 }
-// Before accumulators of mx_group are read by anything but another mx_group:
+// Before accumulators are read by anything but another MFMA:
 // the wait states of the last MFMA.
 __device__ __forceinline__ void mx_settle(v16f (&c)[4])
 {
@@ -207,6 +202,48 @@ __device__ __forceinline__ bool mx_wide_stores(const Mx4GemmArgs& a)
     return (a.N * esz) % 16 == 0 && (uintptr_t)a.out % 16 == 0 && a.N * esz < ((int64_t)1 << 23);
 }
 
+// The biases of this lane, columns c + 32 nt .. + 15 of the n that start at
+// column `first` of expert e's row (zeros from n on).  Loaded all together and
+// waited for here: the compiler's own waits would reach into the K loop.
+template <int NB>
+__device__ __forceinline__ void mx_bias(const Mx4GemmArgs& a, int e, int64_t first, int64_t n, int64_t c, float (&bv)[NB][16])
+{
+    const int dt = a.bias_dtype, esz = dt == F32 ? 4 : 2;
+    const char* p = (const char*)a.bias + ((int64_t)e * a.N + first) * esz;
+    const __amdgpu_buffer_rsrc_t r = mx_rsrc(p, n * esz);
+    const int o = (int)(c * esz);
+    if (dt == F32) {
+#pragma unroll
+        for (int i = 0; i < NB * 16; ++i)
+            bv[i >> 4][i & 15] = __uint_as_float(
+                (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, o + (i >> 4) * 128 + (i & 15) * 4, 0, 0));
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        return;
+    }
+    uint32_t w[NB][8];
+    if (((uintptr_t)p | (uintptr_t)(n * 2)) % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < NB * 2; ++i) {
+            const v4u t = __builtin_bit_cast(
+                v4u, __builtin_amdgcn_raw_buffer_load_b128(r, o + (i >> 1) * 64 + (i & 1) * 16, 0, 0));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[i >> 1][(i & 1) * 4 + k] = t[k];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NB * 8; ++i)
+            w[i >> 3][i & 7] =
+                (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, o + (i >> 3) * 64 + (i & 7) * 4, 0, 0) |
+                (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, o + (i >> 3) * 64 + (i & 7) * 4 + 2, 0, 0) << 16;
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+#pragma unroll
+    for (int i = 0; i < NB * 16; ++i) {
+        const uint16_t h = (uint16_t)(w[i >> 4][(i & 15) >> 1] >> (16 * (i & 1)));
+        bv[i >> 4][i & 15] = dt == BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+    }
+}
+
 // The epilogue of a wave: rows row0 + 32 mt of the tile, sixteen consecutive
 // columns from n0 + c0 + 32 nt in this lane.  Wide stores are range-checked buffer stores, so that every wave issues the same
 // number of them, 4 MT times two (fp32: four), whatever the tile holds.
@@ -219,15 +256,11 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
     const __amdgpu_buffer_rsrc_t ro =
         mx_rsrc((char*)a.out + (m0 * N + n0) * ESZ, ((int64_t)rows * N - n0) * ESZ);
     const uint32_t rstep = (uint32_t)(32 * N * ESZ);
+    float bv[4][16];
+    if (a.bias) mx_bias<4>(a, e, 0, N, n0 + c0, bv);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         const int64_t c = n0 + c0 + 32 * nt;
-        float bv[16];
-        if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                bv[i] = c + i < N ? load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + c + i) : 0.0f;
-        }
         const uint32_t off = (uint32_t)((row0 * N + c0 + 32 * nt) * ESZ);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -237,7 +270,7 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
             for (int i = 0; i < 16; ++i) v[i] = acc[mt][nt][i];
             if (a.bias) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = add_rn(v[i], bv[i]);
+                for (int i = 0; i < 16; ++i) v[i] = add_rn(v[i], bv[nt][i]);
             }
             if (wide) {
                 if constexpr (ODT == F32) {
@@ -268,17 +301,20 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
 
 // ---- the tile kernel ---------------------------------------------------------
 // BM x 256 outputs per workgroup of four waves (2 x 2, each BM/2 x 128), K in
-// steps of 256.
+// steps of 256; one workgroup per CU, which takes tiles in turn.
 //   * A step's codes (128 bytes a row) and scales (8 bytes a row) go global ->
-//     LDS by DMA into one of two slots.  16-byte chunk c of a row sits at
+//     LDS by DMA into one of two slots, two steps ahead of their use and, at a
+//     tile's end, into the next tile's steps.  16-byte chunk c of a row sits at
 //     c ^ swizzle(row): a ds_read_b128 serves sixteen lanes a cycle (lanes
 //     {0-3, 12-15} of one group of sixteen and {4-11} of its neighbour), and
 //     these then hit sixteen different 16-byte bank groups.
-//   * A step is four quarters (t).  While quarter t's MFMAs run from registers,
-//     the fragments of the next one are read from LDS.  Before the last
+//   * A step is four quarters (t).  While one quarter's MFMAs run from
+//     registers, the fragments of the next are read from LDS.  Before the last
 //     quarter the waves wait for the next step's DMA and meet: then nobody
-//     reads this step's slot any more, and the DMA of the step after the next
-//     goes out into it, a whole step ahead of its use.
+//     reads this step's slot any more, and the DMA two steps ahead goes out
+//     into it, half in this quarter and half in the next step's first.
+//     Reads, DMA and addresses are dealt out between the MFMAs, whose 32
+//     cycles each hide them.
 //   * The MFMA takes the weights as first operand, and MFMA row c of a column
 //     tile is column 16 ((c >> 2) & 1) + 4 (c >> 3) + (c & 3), so a lane ends
 //     with sixteen consecutive columns of one row.
@@ -290,9 +326,13 @@ template <int BM, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int tiles_m, int tiles_n)
 {
     constexpr int MT = BM / 64, NT = 4;       // 32 x 32 tiles per wave
+    // a slot: codes and scales of both operands (256 bytes more for the scale
+    // DMA of waves that have no rows, so that all issue the same)
     constexpr int AB = BM * 128, BB = 256 * 128, SAB = BM * 8, SBB = 256 * 8;
-    constexpr int SLOT = AB + BB + SAB + SBB;
+    constexpr int SLOT = AB + BB + SAB + SBB + (BM == 64 ? 256 : 0);
     constexpr int AI = BM / 32;               // A DMA instructions per wave (8 rows each)
+    constexpr int SAI = BM == 256 ? 2 : 1;    // of A's scales (32 rows each)
+    constexpr int DMAS = AI + 8 + SAI + 2;    // all of a step's, per wave
     __shared__ __align__(16) uint8_t smem[2 * SLOT];
 
     const int tid = threadIdx.x;
@@ -301,7 +341,6 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     const int wm = wave & 1, wn = wave >> 1;
     const int64_t K = a.K, N = a.N, pitch = K >> 1;
     const int nsteps = (int)((K + 255) / 256);
-
     const int kblocks = (int)(K >> 5);
     const int64_t F = N >> 1;   // gated: number of results
 
@@ -347,90 +386,85 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     };
 
     // ---- DMA: wave w moves rows [w BM/4, (w + 1) BM/4) of A and 64 weight columns
-    const int l8 = lane >> 3, c8 = lane & 7;
-    const int ar0 = wave * (BM / 4);
-    // (bits 1 and 2 of the row; bit 3, for columns bit 4, is the instruction's)
-    const int cs = c8 ^ (l8 >> 1);
+    const int l8 = lane >> 3, ar0 = wave * (BM / 4);
+    // chunk of this lane (bits 1 and 2 of the row decide; bit 3, for columns
+    // bit 4, is the instruction's and turns it into its partner ^ 4)
+    const int ch = (lane & 7) ^ (l8 >> 1);
     const bool gather = GROUPED && a.rows != nullptr;
-    const int64_t srows = a.M;               // rows of a scale slab
-    const uint32_t bvo = (uint32_t)(l8 * pitch), bstep = (uint32_t)(8 * pitch);
-    // of the tile whose steps are being moved:
-    uint32_t avo[AI], savo[2];               // lane offsets of rows and of their scales
-    __amdgpu_buffer_rsrc_t ra, rb;           // codes; empty where there is no tile
-    const uint8_t *sabase, *sbcol;           // scales
-    int64_t sabytes, sbbytes;
+    // Every resource is 2^31 bytes long: a lane that has nothing to read (a row
+    // or column past the tile's, no tile, a chunk past K) has an offset past
+    // that and gets zeros.
+    const int slab_a = (int)(a.M * 8), slab_b = (int)(N * 8);   // bytes of a scale slab
+    uint32_t avo[AI], bvo[8], savo[SAI], sbvo[2];   // lane offsets of codes and scales
+    __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
     auto set_dma = [&](const Tile& t) {
-        // the source row of tile row i, or one past the resource
+        // the source row of tile row i, or none
         auto src_row = [&](int i) -> int64_t {
-            if (!gather) return i;
             if (i >= t.rows) return -1;
+            if (!gather) return i;
             const int64_t s = a.rows[t.m0 + i];
             return s >= 0 && s < a.M ? s : -1;
         };
 #pragma unroll
         for (int i = 0; i < AI; ++i) {
             const int64_t s = src_row(ar0 + 8 * i + l8);
-            avo[i] = s < 0 ? kOut : (uint32_t)(s * pitch);
+            avo[i] = s < 0 ? kOut : (uint32_t)(s * pitch + (ch ^ ((i & 1) * 4)) * 16);
         }
-        // scales: 32 rows per 64-lane instruction; BM / 32 instructions in all
+        // scales: 32 rows per instruction, two words each
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r0 = BM == 256 ? wave * 64 + i * 32 : wave * 32;
-            const int64_t s = src_row(r0 + (lane >> 1));
-            savo[i] = s < 0 || r0 >= BM ? kOut : (uint32_t)(s * 8 + (lane & 1) * 4);
+        for (int i = 0; i < SAI; ++i) {
+            const int r0 = wave * 32 * SAI + i * 32;
+            const int64_t s = r0 < BM ? src_row(r0 + (lane >> 1)) : -1;
+            savo[i] = s < 0 ? kOut : (uint32_t)(s * 8 + (lane & 1) * 4);
         }
-        const int64_t arows = t.rows == 0 ? 0 : gather ? a.M : t.rows;   // rows behind the resource
-        ra = mx_rsrc(gather ? a.a : a.a + t.m0 * pitch, arows * pitch);
-        sabase = gather ? a.sa : a.sa + t.m0 * 8;
-        sabytes = arows * 8;
+        ra = mx_rsrc(gather ? a.a : a.a + t.m0 * pitch, kOut);
+        rsa = mx_rsrc(gather ? a.sa : a.sa + t.m0 * 8, kOut);
         // the wave's 64 weight columns (gated: even waves gates, odd waves ups)
         const int64_t col0 = GATED ? (int64_t)t.tn * 128 + (wave >> 1) * 64 : (int64_t)t.tn * 256 + wave * 64;
         const int64_t ncols = t.rows == 0 ? 0 : GATED ? F : N;
-        const int64_t left = ncols - col0 < 0 ? 0 : ncols - col0 > 64 ? 64 : ncols - col0;
+        const int left = (int)(ncols - col0 < 0 ? 0 : ncols - col0 > 64 ? 64 : ncols - col0);
         const int64_t wcol = left == 0 ? 0 : GATED ? (wave & 1) * F + col0 : col0;
-        rb = mx_rsrc(a.b + ((int64_t)t.e * N + wcol) * pitch, left * pitch);
-        sbcol = a.sb + ((int64_t)t.e * nsteps * N + wcol) * 8;
-        sbbytes = left * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            bvo[i] = 8 * i + l8 < left ? (uint32_t)((8 * i + l8) * pitch + (ch ^ ((i & 2) * 2)) * 16) : kOut;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sbvo[i] = 32 * i + (lane >> 1) < left ? lane * 4u + i * 256u : kOut;
+        rb = mx_rsrc(a.b + ((int64_t)t.e * N + wcol) * pitch, kOut);
+        rsb = mx_rsrc(a.sb + ((int64_t)t.e * nsteps * N + wcol) * 8, kOut);
     };
 
     // The DMA of one step, an instruction at a time: `Dma` holds what its
     // instructions share.
-    constexpr int SAI = BM == 256 ? 2 : 1, DMAS = AI + 8 + SAI + 2;
     struct Dma {
-        uint8_t* sl;
-        int ko;
-        uint32_t t0, t1;   // chunk cs and its partner cs ^ 4
-        __amdgpu_buffer_rsrc_t rsa, rsb;
+        int ko, soa, sob;    // offsets of the step in a row of codes and in the scales
+        uint32_t t0, t1;     // kOut where the chunk, its partner lies past K
     };
-    auto dma_of = [&](int slot, int s) {
-        // chunks past K read zeros (offset past the resource)
-        return Dma{smem + slot * SLOT, s * 128, s * 8 + cs < kblocks ? cs * 16u : kOut,
-                   s * 8 + (cs ^ 4) < kblocks ? (cs ^ 4) * 16u : kOut, mx_rsrc(sabase + s * srows * 8, sabytes),
-                   mx_rsrc(sbcol + s * N * 8, sbbytes)};
+    auto dma_chunks = [&](Dma& d, int s) {
+        d.t0 = s * 8 < kblocks - ch ? 0u : kOut;
+        d.t1 = s * 8 < kblocks - (ch ^ 4) ? 0u : kOut;
     };
-    auto dma = [&](const Dma& d, int n) {
+    auto dma_offsets = [&](Dma& d, int s) {
+        d.ko = s * 128;
+        d.soa = s * slab_a;
+        d.sob = s * slab_b;
+    };
+    auto dma = [&](const Dma& d, int sl, int n) {
         if (n < AI) {
-            // (a row offset or a chunk past the resource stays past it: both
-            // are below 2^31 otherwise)
-            const uint32_t c = (n & 1) ? d.t1 : d.t0, r = avo[n < AI ? n : 0];
-            mx_dma<16>(ra, d.sl + (ar0 + 8 * n) * 128, (r + (c & ~kOut)) | ((r | c) & kOut), d.ko);
+            mx_dma<16>(ra, smem + sl + (ar0 + 8 * n) * 128, avo[n < AI ? n : 0] | ((n & 1) ? d.t1 : d.t0), d.ko);
         } else if (n < AI + 8) {
             const int i = n - AI;
-            mx_dma<16>(rb, d.sl + AB + (wave * 64 + 8 * i) * 128, ((i & 2) ? d.t1 : d.t0) + bvo + i * bstep, d.ko);
+            mx_dma<16>(rb, smem + sl + AB + (wave * 64 + 8 * i) * 128, bvo[i & 7] | ((i & 2) ? d.t1 : d.t0), d.ko);
         } else if (n < AI + 8 + SAI) {
-            const int i = n - AI - 8;
-            if constexpr (BM == 256)
-                mx_dma<4>(d.rsa, d.sl + AB + BB + (wave * 64 + i * 32) * 8, savo[i & 1], 0);
-            else if (wave * 32 < BM)
-                mx_dma<4>(d.rsa, d.sl + AB + BB + wave * 32 * 8, savo[0], 0);
+            const int i = n - AI - 8, r0 = wave * 32 * SAI + i * 32;
+            mx_dma<4>(rsa, smem + sl + AB + BB + (r0 < BM ? r0 * 8 : SAB + SBB), savo[i < SAI ? i : 0], d.soa);
         } else {
             const int i = n - AI - 8 - SAI;
-            mx_dma<4>(d.rsb, d.sl + AB + BB + SAB + (wave * 64 + i * 32) * 8, lane * 4 + i * 256, 0);
+            mx_dma<4>(rsb, smem + sl + AB + BB + SAB + (wave * 64 + i * 32) * 8, sbvo[i & 1], d.sob);
         }
     };
-    // The steps of all tiles form one sequence; the DMA runs up to two steps,
-    // so up to two tiles, ahead of the MFMAs.
-    Tile cur = tile_of(blockIdx.x), q1{0, 0, 0, 0}, q2{0, 0, 0, 0};
+    // The steps of all tiles form one sequence; the DMA runs two steps, so up
+    // to two tiles, ahead of the MFMAs.
+    Tile cur = tile_of(blockIdx.x), q0{0, 0, 0, 0}, q1 = q0;
     if (cur.rows == 0) return;
     int64_t t_dma = blockIdx.x;
     int s_dma = 0, ahead = 0;
@@ -441,13 +475,16 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
         t_dma += gridDim.x;
         const Tile t = tile_of(t_dma);
         set_dma(t);
-        (ahead == 0 ? q1 : q2) = t;
+        // (by value: a choice of addresses would put the queue in memory)
+        auto put = [&](Tile& q, bool here) {
+            q.m0 = here ? t.m0 : q.m0;
+            q.rows = here ? t.rows : q.rows;
+            q.tn = here ? t.tn : q.tn;
+            q.e = here ? t.e : q.e;
+        };
+        put(q0, ahead == 0);
+        put(q1, ahead == 1);
         ++ahead;
-    };
-    auto issue = [&](int slot) {
-        const Dma d = dma_of(slot, s_dma);
-#pragma unroll
-        for (int n = 0; n < DMAS; ++n) dma(d, n);
     };
 
     // ---- fragments: row tile mt is rows arow + 32 mt, column tile nt columns
@@ -459,7 +496,8 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     const int so_a = AB + BB + arow * 8 + 4 * h, so_b = AB + BB + SAB + bcol * 8 + 4 * h;
     v4i fa[2][MT], fb[2][NT];            // fragments of two quarters
     uint32_t fsa[MT], fsb[NT], nsa[MT], nsb[NT];   // scale words of this step and the next
-    // fragment i of quarter t, in the order of first use; scale word i of a step
+    constexpr int FR = MT + NT;
+    constexpr int NM = MT * NT, NR = NM < FR ? NM : FR;   // MFMAs of a quarter; the first NR are followed by reads
     auto read = [&](int sl, int t, int i) {
         if (i < NT) fb[t & 1][i] = *(const v4i*)(smem + ((sl + bo) ^ (t * 16)) + i * 32 * 128);
         else fa[t & 1][i - NT] = *(const v4i*)(smem + ((sl + ao) ^ (t * 16)) + (i - NT) * 32 * 128);
@@ -468,60 +506,78 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
         if (i < NT) nsb[i] = *(const uint32_t*)(smem + sl + so_b + i * 32 * 8);
         else nsa[i - NT] = *(const uint32_t*)(smem + sl + so_a + (i - NT) * 32 * 8);
     };
-    constexpr int FR = MT + NT;
+    // the fragments that follow MFMA k of a quarter: of quarter t of a slot
+    auto reads_at = [&](int sl, int t, int k, bool scales) {
+        if (k >= NR) return;
+#pragma unroll
+        for (int i = k * FR / NR; i < (k + 1) * FR / NR; ++i) {
+            read(sl, t, i);
+            if (scales) read_scale(sl, i);
+        }
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) fsb[i] = nsb[i];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) fsa[i] = nsa[i];
+    };
 
-    issue(0);
-    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        Dma d;
+        dma_chunks(d, s_dma);
+        dma_offsets(d, s_dma);
+#pragma unroll
+        for (int n = 0; n < DMAS; ++n) dma(d, s * SLOT, n);
+        if (s == 0) advance();
+    }
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DMAS) : "memory");   // the first step has landed
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    advance();
-    issue(1);
 #pragma unroll
     for (int i = 0; i < FR; ++i) {
         read(0, 0, i);
         read_scale(0, i);
     }
-    // A quarter: MT groups of four MFMAs; behind each, its share of the next
-    // quarter's fragment reads, and in the last quarter of the next step's
-    // scale words and of the DMA, under the MFMAs' time
     const int row0 = wm * (BM / 2) + j;    // this lane's row (+ 32 mt), and of the
     const int c0 = wn * 128 + 16 * h;      // columns sixteen from c0 + 32 nt
     const bool wide = !GATED && mx_wide_stores(a);
-    int slot = 0, stores = 0;              // stores: the last epilogue's, if they may stay in flight
+    constexpr int D1 = DMAS / 2;           // DMA instructions of the last quarter; the others follow
+    int sl = 0, stores = 0;                // stores: whether the last epilogue's may be in flight
+    Dma d;
     for (;;) {
         v16f acc[MT][NT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) mx_clear(acc[mt]);
-        for (int s = 0; s < nsteps; ++s) {
-            const int cur_s = slot * SLOT, nxt_s = SLOT - cur_s;
+        // the first quarter of the tile's first step (its DMA went out before
+        // the last epilogue)
+        take_scales();
 #pragma unroll
-            for (int i = 0; i < NT; ++i) fsb[i] = nsb[i];
+        for (int k = 0; k < NM; ++k) {
+            mx_mma<0>(acc[k / NT][k % NT], fb[0][k % NT], fa[0][k / NT], fsb[k % NT], fsa[k / NT]);
+            reads_at(sl, 1, k, false);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int s = 0;;) {
+            const int nx = SLOT - sl;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) fsa[i] = nsa[i];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                mx_group<0>(acc[mt], fb[0], fa[0][mt], fsb, fsa[mt]);
-#pragma unroll
-                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) read(cur_s, 1, i);
+            for (int k = 0; k < NM; ++k) {
+                mx_mma<1>(acc[k / NT][k % NT], fb[1][k % NT], fa[1][k / NT], fsb[k % NT], fsa[k / NT]);
+                reads_at(sl, 2, k, false);
+                if (k == NM / 2) advance();
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                mx_group<1>(acc[mt], fb[1], fa[1][mt], fsb, fsa[mt]);
-#pragma unroll
-                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) read(cur_s, 2, i);
+            for (int k = 0; k < NM; ++k) {
+                mx_mma<2>(acc[k / NT][k % NT], fb[0][k % NT], fa[0][k / NT], fsb[k % NT], fsa[k / NT]);
+                reads_at(sl, 3, k, false);
+                if (k == NM / 2) dma_chunks(d, s_dma);
+                if (k == NM * 3 / 4) dma_offsets(d, s_dma);
                 __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                mx_group<2>(acc[mt], fb[0], fa[0][mt], fsb, fsa[mt]);
-#pragma unroll
-                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) read(cur_s, 3, i);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            // The next step has landed, this one is read.  Its DMA went out before
-            // the previous tile's stores, which may stay in flight in a tile's
-            // first step.
+            // The next step has landed (in a tile's first step all but the
+            // stores of the tile before, which went out after it), and this
+            // one is read.
             asm volatile("s_waitcnt lgkmcnt(0)\n\t"
                          "s_cmp_eq_u32 %0, 0\n\t"
                          "s_cbranch_scc1 1f\n\t"
@@ -534,40 +590,45 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
-            advance();
-            const Dma d = dma_of(slot, s_dma);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                mx_group<3>(acc[mt], fb[1], fa[1][mt], fsb, fsa[mt]);
+            for (int k = 0; k < NM; ++k) {
+                mx_mma<3>(acc[k / NT][k % NT], fb[1][k % NT], fa[1][k / NT], fsb[k % NT], fsa[k / NT]);
+                reads_at(nx, 0, k, true);   // (past the last step: of a slot's older contents, unused)
 #pragma unroll
-                for (int i = mt * DMAS / MT; i < (mt + 1) * DMAS / MT; ++i) dma(d, i);
-#pragma unroll
-                for (int i = mt * FR / MT; i < (mt + 1) * FR / MT; ++i) {
-                    read(nxt_s, 0, i);   // (past the last step: of an older one, unused)
-                    read_scale(nxt_s, i);
-                }
+                for (int i = k * D1 / NM; i < (k + 1) * D1 / NM; ++i) dma(d, sl, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            slot ^= 1;
+            if (++s == nsteps) break;
+            take_scales();
+#pragma unroll
+            for (int k = 0; k < NM; ++k) {
+                mx_mma<0>(acc[k / NT][k % NT], fb[0][k % NT], fa[0][k / NT], fsb[k % NT], fsa[k / NT]);
+                reads_at(nx, 1, k, false);
+#pragma unroll
+                for (int i = D1 + k * (DMAS - D1) / NM; i < D1 + (k + 1) * (DMAS - D1) / NM; ++i) dma(d, sl, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            sl = nx;
         }
+#pragma unroll
+        for (int i = D1; i < DMAS; ++i) dma(d, sl, i);
+        sl = SLOT - sl;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) mx_settle(acc[mt]);
 
         // ---- epilogue
         if constexpr (GATED) {
             const int64_t R = GROUPED ? a.R : a.M;
+            const int64_t fw = (int64_t)cur.tn * 128 + wn * 64 + 16 * h;
+            float bg[2][16], bu[2][16];
+            if (a.bias) {
+                mx_bias<2>(a, cur.e, 0, F, fw, bg);
+                mx_bias<2>(a, cur.e, F, F, fw, bu);
+            }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const int64_t f0 = (int64_t)cur.tn * 128 + wn * 64 + 32 * nt + 16 * h;
+                const int64_t f0 = fw + 32 * nt;
                 const bool in_f = f0 < F;     // F is a multiple of 32, so are the blocks
-                float bg[16], bu[16];
-                if (a.bias) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        bg[i] = in_f ? load_any_f32(a.bias_dtype, a.bias, (int64_t)cur.e * N + f0 + i) : 0.0f;
-                        bu[i] = in_f ? load_any_f32(a.bias_dtype, a.bias, (int64_t)cur.e * N + F + f0 + i) : 0.0f;
-                    }
-                }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     float v[16];
@@ -578,8 +639,8 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
                     for (int i = 0; i < 16; ++i) {
                         float g = acc[mt][nt][i], u = acc[mt][2 + nt][i];
                         if (a.bias) {
-                            g = add_rn(g, bg[i]);
-                            u = add_rn(u, bu[i]);
+                            g = add_rn(g, bg[nt][i]);
+                            u = add_rn(u, bu[nt][i]);
                         }
                         v[i] = mx_gated(g, u);
                         m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
@@ -616,10 +677,10 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             if (a.out_dtype == BF16) mx_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
             else if (a.out_dtype == F16) mx_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
             else mx_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
-            stores = wide && !a.bias;   // (bias loads wait for what went before them)
+            stores = wide;
         }
-        cur = q1;
-        q1 = q2;
+        cur = q0;
+        q0 = q1;
         --ahead;
         if (cur.rows == 0) break;
     }
