@@ -125,12 +125,14 @@ template <int BM, bool BY_TILE> __device__ __forceinline__ int64_t mx_find(const
         }
         const int cnt = hi > lo ? (int)(hi - lo) : 0;
         const int cm = (cnt + BM - 1) / BM;
+        // inclusive scan over the lanes: within rows of sixteen, then across
         int inc = cm;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int v = __shfl_up(inc, d);
-            if (lane >= d) inc += v;
-        }
+        inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+        inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xf, 0xf, false);
+        inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xf, 0xf, false);
+        inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xf, 0xf, false);
+        inc += __builtin_amdgcn_update_dpp(0, inc, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
+        inc += __builtin_amdgcn_update_dpp(0, inc, 0x143, 0xc, 0xf, false);
         const int sum = __builtin_amdgcn_readlane(inc, 63);
         if (BY_TILE && r.e < 0 && idx >= base * per && idx < (base + sum) * per) {
             const unsigned long long hit = __ballot((base + inc) * per > idx);
@@ -688,19 +690,24 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 
 // ---- the skinny kernel -------------------------------------------------------
 // Few rows: the weights are the cost, read once, straight into registers.  A
-// workgroup of eight waves takes 16 MT rows and 16 columns (gated: 32 gates
-// and their 32 ups, one block of results); the waves share the K steps and
-// their partial sums meet in LDS, added in wave order.
+// workgroup of eight waves takes 16 MT rows.  KW of its waves share the K
+// steps of one group of 16 NT columns (gated, NT = 4: 32 gates and their 32
+// ups, one block of results); 8 / KW groups lie side by side.  The waves'
+// partial sums meet in LDS and are added in wave order.
 constexpr int kSkinnyWaves = 8;
-template <int MT, bool GROUPED, bool GATED>
+template <int MT, int NT, int KW, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
 {
-    constexpr int NT = GATED ? 4 : 1, W = kSkinnyWaves;
-    __shared__ float part[W][MT][NT][16][17];   // [wave][row tile][column tile][row][column]
+    static_assert(!GATED || NT == 4, "a block of gates and its ups");
+    constexpr int W = kSkinnyWaves, CG = W / KW;
+    constexpr int COLS = GATED ? 32 : 16 * NT;   // results of a column group
+    __shared__ float part[W][MT][NT][16][17];    // [wave][row tile][column tile][row][column]
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int kw = wave % KW, cg = wave / KW;
     const int j = lane & 15, q = lane >> 4;
     const int64_t K = a.K, N = a.N, F = N >> 1, pitch = K >> 1;
+    const int64_t n = GATED ? F : N;             // results of a row
     const int nsteps = (int)((K + 255) / 256);
     int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
     int rows, e = 0;
@@ -721,13 +728,13 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
     const uint8_t* wb = a.b + (int64_t)e * N * pitch;
     const uint8_t* wsb = a.sb + (int64_t)e * nsteps * N * 8;
     const int kblocks = (int)(K >> 5);
+    const int64_t first = ((int64_t)blockIdx.x * CG + cg) * COLS;   // the group's first result
     // this lane's weight columns and rows (clamped: what they give is not stored)
     int64_t col[NT], src[MT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int64_t c = GATED ? (int64_t)blockIdx.x * 32 + (nt & 1) * 16 + j : (int64_t)blockIdx.x * 16 + j;
-        const int64_t n = GATED ? F : N;
-        col[nt] = (c < n ? c : n - 1) + (nt >> 1) * F;
+        const int64_t c = first + (GATED ? (nt & 1) : nt) * 16 + j;
+        col[nt] = (c < n ? c : n - 1) + (GATED ? (nt >> 1) * F : 0);
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -745,13 +752,13 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = (v4f){0.f, 0.f, 0.f, 0.f};
-    constexpr int U = GATED ? 1 : 2;     // steps in flight
-    for (int s0 = wave; s0 < nsteps; s0 += W * U) {
+    constexpr int U = NT * MT > 4 ? 1 : 2;     // steps in flight
+    for (int s0 = kw; s0 < nsteps; s0 += KW * U) {
         v4i fb[U][NT][2], fa[U][MT][2];
         uint32_t sb[U][NT], sa[U][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int s = s0 + W * u;
+            const int s = s0 + KW * u;
             const bool in = s < nsteps;
             const int b0 = s * 8 + 2 * q;        // this lane's two blocks
 #pragma unroll
@@ -788,19 +795,21 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
 #pragma unroll
             for (int r = 0; r < 4; ++r) part[wave][mt][nt][j][4 * q + r] = acc[mt][nt][r];
     __syncthreads();
-    const int waves = nsteps < W ? nsteps : W;
-    auto sum = [&](int mt, int nt, int row, int c) {
-        float v = part[0][mt][nt][row][c];
-        for (int w = 1; w < waves; ++w) v = add_rn(v, part[w][mt][nt][row][c]);
+    const int waves = nsteps < KW ? nsteps : KW;   // those that had a step
+    auto sum = [&](int g, int mt, int nt, int row, int c) {
+        float v = part[g * KW][mt][nt][row][c];
+        for (int w = 1; w < waves; ++w) v = add_rn(v, part[g * KW + w][mt][nt][row][c]);
         return v;
     };
     if constexpr (GATED) {
-        // a half wave takes the 32 results of one row
+        // a half wave takes the 32 results of one row of one group
         const int c = tid & 31;
-        const int64_t f = (int64_t)blockIdx.x * 32 + c, R = GROUPED ? a.R : a.M;
-        for (int row = tid >> 5; row < 16 * MT; row += 16) {
-            const int mt = row >> 4;
-            float g = sum(mt, c >> 4, row & 15, c & 15), u = sum(mt, 2 + (c >> 4), row & 15, c & 15);
+        const int64_t R = GROUPED ? a.R : a.M;
+        for (int i = tid >> 5; i < 16 * MT * CG; i += 16) {
+            const int row = i % (16 * MT), g_ = i / (16 * MT), mt = row >> 4;
+            const int64_t f = ((int64_t)blockIdx.x * CG + g_) * 32 + c;
+            if (f >= F || row >= rows) continue;   // (whole half waves)
+            float g = sum(g_, mt, c >> 4, row & 15, c & 15), u = sum(g_, mt, 2 + (c >> 4), row & 15, c & 15);
             if (a.bias) {
                 g = add_rn(g, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + f));
                 u = add_rn(u, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + F + f));
@@ -813,26 +822,25 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
             const float hi = __shfl_down(v, 1);
             uint32_t cc = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, hi, __uint_as_float(byte << 23), 0);
             if (byte == 255) cc = 0;
-            if (row < rows) {
-                if (!(c & 1)) a.out_codes[((m0 + row) * F + f) / 2] = (uint8_t)cc;
-                if (c == 0) {
-                    const int64_t blk = f >> 5;
-                    uint8_t* o = a.out_scales + ((blk >> 3) * R + m0 + row) * 8;
-                    o[blk & 7] = (uint8_t)byte;
-                    // the last block also clears what is left of its slab
-                    if (blk == (F >> 5) - 1)
-                        for (int b = (int)(blk & 7) + 1; b < 8; ++b) o[b] = 0;
-                }
+            if (!(c & 1)) a.out_codes[((m0 + row) * F + f) / 2] = (uint8_t)cc;
+            if (c == 0) {
+                const int64_t blk = f >> 5;
+                uint8_t* o = a.out_scales + ((blk >> 3) * R + m0 + row) * 8;
+                o[blk & 7] = (uint8_t)byte;
+                // the last block also clears what is left of its slab
+                if (blk == (F >> 5) - 1)
+                    for (int b = (int)(blk & 7) + 1; b < 8; ++b) o[b] = 0;
             }
         }
     } else {
-        for (int i = tid; i < MT * 256; i += 512) {
-            const int mt = i >> 8, row = (i >> 4) & 15, c = i & 15;
-            const int64_t n = (int64_t)blockIdx.x * 16 + c;
-            float v = sum(mt, 0, row, c);
-            if (n < N && 16 * mt + row < rows) {
-                if (a.bias) v = add_rn(v, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + n));
-                store_any(a.out_dtype, a.out, (m0 + 16 * mt + row) * N + n, v);
+        constexpr int WG = CG * COLS;
+        for (int i = tid; i < 16 * MT * WG; i += 512) {
+            const int row = i / WG, c = i % WG, g = c / COLS, nt = (c % COLS) >> 4;
+            const int64_t nn = (int64_t)blockIdx.x * WG + c;
+            if (nn < N && row < rows) {
+                float v = sum(g, row >> 4, nt, row & 15, c & 15);
+                if (a.bias) v = add_rn(v, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + nn));
+                store_any(a.out_dtype, a.out, (m0 + row) * N + nn, v);
             }
         }
     }
@@ -857,21 +865,30 @@ template <int BM> hipError_t launch_tile(const Mx4GemmArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int MT> hipError_t launch_skinny(const Mx4GemmArgs& a, hipStream_t st)
+template <int MT, int NT, int KW, bool GATED> hipError_t launch_skinny_w(const Mx4GemmArgs& a, hipStream_t st)
 {
-    const bool gated = a.out_codes != nullptr;
-    const unsigned tn = (unsigned)(gated ? a.N / 64 : (a.N + 15) / 16);
+    constexpr int COLS = (GATED ? 32 : 16 * NT) * (kSkinnyWaves / KW);
+    const int64_t n = GATED ? a.N / 2 : a.N;
+    const unsigned tn = (unsigned)((n + COLS - 1) / COLS);
     if (a.E) {
         const unsigned tm = (unsigned)(a.R / (16 * MT) + (a.E < a.R ? a.E : a.R) + 1);
-        if (gated)
-            hipLaunchKernelGGL((mx4_skinny_kernel<MT, true, true>), dim3(tn, tm), dim3(512), 0, st, a);
-        else
-            hipLaunchKernelGGL((mx4_skinny_kernel<MT, true, false>), dim3(tn, tm), dim3(512), 0, st, a);
-    } else {
-        hipLaunchKernelGGL((mx4_skinny_kernel<MT, false, false>), dim3(tn, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
+        hipLaunchKernelGGL((mx4_skinny_kernel<MT, NT, KW, true, GATED>), dim3(tn, tm), dim3(512), 0, st, a);
+    } else if constexpr (!GATED) {
+        hipLaunchKernelGGL((mx4_skinny_kernel<MT, NT, KW, false, false>), dim3(tn, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
                            dim3(512), 0, st, a);
     }
     return hipGetLastError();
+}
+
+template <int MT> hipError_t launch_skinny(const Mx4GemmArgs& a, hipStream_t st)
+{
+    // half the waves per column group where K has few steps for eight of them
+    const bool deep = a.K > 1792;
+    if (a.out_codes) return deep ? launch_skinny_w<MT, 4, 8, true>(a, st) : launch_skinny_w<MT, 4, 4, true>(a, st);
+    // 32 columns a group once 16 would make more workgroups than the CUs hold
+    const bool narrow = !a.E && (a.N + 15) / 16 * ((a.M + 16 * MT - 1) / (16 * MT)) <= 512;
+    if (narrow) return deep ? launch_skinny_w<MT, 1, 8, false>(a, st) : launch_skinny_w<MT, 1, 4, false>(a, st);
+    return deep ? launch_skinny_w<MT, 2, 8, false>(a, st) : launch_skinny_w<MT, 2, 4, false>(a, st);
 }
 
 }  // namespace
@@ -894,7 +911,7 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t st)
     case kMx4Tile64: return launch_tile<64>(a, st);
     }
     const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
-    return rows <= 16 ? launch_skinny<1>(a, st) : launch_skinny<2>(a, st);
+    return rows <= 16 ? launch_skinny<1>(a, st) : rows <= 32 ? launch_skinny<2>(a, st) : launch_skinny<4>(a, st);
 }
 
 }  // namespace w4a4
