@@ -31,6 +31,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void* base, int6
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)n, 0x00020000);
 }
 
+// A pointer that is the same in all lanes, where the compiler cannot tell: its
+// resource stays in scalar registers (otherwise each access becomes a loop).
+__device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p)
+{
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return (const uint8_t*)((uint64_t)hi << 32 | lo);
+}
+
 // BYTES per lane from the resource (lane offset vo, scalar offset so; nothing
 // past its end: zeros) to consecutive LDS bytes
 template <int BYTES> __device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t vo, int so)
@@ -106,6 +116,18 @@ __device__ __forceinline__ int64_t mx_offset(const Mx4GemmArgs& a, int e)
     return o < 0 ? 0 : o > a.R ? a.R : o;
 }
 
+// inclusive sum over the lanes: within rows of sixteen, then across
+__device__ __forceinline__ int mx_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
+}
+
 // The row tile `idx` of the list of all experts' tiles of BM rows (idx < 0:
 // only count).  Every wave scans the offsets, 64 experts at a time.  Returns
 // the number of tiles.
@@ -125,14 +147,7 @@ template <int BM, bool BY_TILE> __device__ __forceinline__ int64_t mx_find(const
         }
         const int cnt = hi > lo ? (int)(hi - lo) : 0;
         const int cm = (cnt + BM - 1) / BM;
-        // inclusive scan over the lanes: within rows of sixteen, then across
-        int inc = cm;
-        inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
-        inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xf, 0xf, false);
-        inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xf, 0xf, false);
-        inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xf, 0xf, false);
-        inc += __builtin_amdgcn_update_dpp(0, inc, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
-        inc += __builtin_amdgcn_update_dpp(0, inc, 0x143, 0xc, 0xf, false);
+        const int inc = mx_scan(cm);
         const int sum = __builtin_amdgcn_readlane(inc, 63);
         if (BY_TILE && r.e < 0 && idx >= base * per && idx < (base + sum) * per) {
             const unsigned long long hit = __ballot((base + inc) * per > idx);
@@ -147,6 +162,44 @@ template <int BM, bool BY_TILE> __device__ __forceinline__ int64_t mx_find(const
         base += sum;
     }
     return base;
+}
+
+// For each lane, row tile and column tile number `tile` of the list of all
+// experts' tiles (BM rows by one of tiles_n column tiles): within an expert,
+// groups of eight row tiles, row tiles fastest.
+template <int BM>
+__device__ __forceinline__ void mx_rows_of(const Mx4GemmArgs& a, int tile, int tiles_n, int& e, int& m0, int& tn, int& rows)
+{
+    const int lane = threadIdx.x & 63, row_tile = tile / tiles_n;
+    int base = 0;
+    e = m0 = tn = rows = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        int lo = 0, hi = 0;
+        if (e0 + lane < a.E) {
+            lo = (int)mx_offset(a, e0 + lane);
+            hi = (int)mx_offset(a, e0 + lane + 1);
+        }
+        const int cnt = hi > lo ? hi - lo : 0, cm = (cnt + BM - 1) / BM, inc = mx_scan(cm);
+        const int sum = __builtin_amdgcn_readlane(inc, 63);
+        // the first expert whose tiles reach past row_tile
+        const int x = row_tile - base;
+        int w = 0;
+#pragma unroll
+        for (int d = 32; d; d >>= 1)
+            if (__builtin_amdgcn_ds_bpermute((w + d - 1) * 4, inc) <= x) w += d;
+        w = min(w, 63);
+        const int wlo = __builtin_amdgcn_ds_bpermute(w * 4, lo), wcnt = __builtin_amdgcn_ds_bpermute(w * 4, cnt);
+        const int wcm = __builtin_amdgcn_ds_bpermute(w * 4, cm), winc = __builtin_amdgcn_ds_bpermute(w * 4, inc);
+        if (x >= 0 && x < sum) {
+            const int in_e = tile - (base + winc - wcm) * tiles_n, per = 8 * tiles_n, grp = in_e / per;
+            const int gm = min(wcm - grp * 8, 8), in_g = in_e - grp * per, m = grp * 8 + in_g % gm;
+            e = e0 + w;
+            tn = in_g / gm;
+            m0 = wlo + m * BM;
+            rows = min(wcnt - m * BM, BM);
+        }
+        base += sum;
+    }
 }
 
 // Zeros for the sorted rows that no expert owns (from offsets[E] on), spread
@@ -211,7 +264,7 @@ template <int NB>
 __device__ __forceinline__ void mx_bias(const Mx4GemmArgs& a, int e, int64_t first, int64_t n, int64_t c, float (&bv)[NB][16])
 {
     const int dt = a.bias_dtype, esz = dt == F32 ? 4 : 2;
-    const char* p = (const char*)a.bias + ((int64_t)e * a.N + first) * esz;
+    const uint8_t* p = mx_uniform((const uint8_t*)a.bias + ((int64_t)e * a.N + first) * esz);
     const __amdgpu_buffer_rsrc_t r = mx_rsrc(p, n * esz);
     const int o = (int)(c * esz);
     if (dt == F32) {
@@ -256,7 +309,7 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
     constexpr int ESZ = ODT == F32 ? 4 : 2;
     const int64_t N = a.N;
     const __amdgpu_buffer_rsrc_t ro =
-        mx_rsrc((char*)a.out + (m0 * N + n0) * ESZ, ((int64_t)rows * N - n0) * ESZ);
+        mx_rsrc(mx_uniform((const uint8_t*)a.out + (m0 * N + n0) * ESZ), ((int64_t)rows * N - n0) * ESZ);
     const uint32_t rstep = (uint32_t)(32 * N * ESZ);
     float bv[4][16];
     if (a.bias) mx_bias<4>(a, e, 0, N, n0 + c0, bv);
@@ -348,43 +401,43 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 
     // ---- tiles: this workgroup takes number blockIdx.x, + gridDim.x, ...
     struct Tile {
-        int64_t m0;
-        int rows, tn, e;   // rows 0: none
+        int m0, rows, tn, e;   // rows 0: none
     };
-    int64_t ntiles;
+    int ntiles;
     if constexpr (GROUPED) {
         MxRows r;
-        ntiles = mx_find<BM, false>(a, 0, 1, r) * tiles_n;
+        ntiles = (int)mx_find<BM, false>(a, 0, 1, r) * tiles_n;
         mx_zero_rows(a, blockIdx.x, gridDim.x);
     } else {
-        ntiles = (int64_t)tiles_m * tiles_n;
+        ntiles = tiles_m * tiles_n;
     }
-    auto tile_of = [&](int64_t t) {
-        Tile r{0, 0, 0, 0};
-        if (t >= ntiles) return r;
+    // Lane i of every wave holds the workgroup's i-th tile of a batch of 64:
+    // looking tiles up one at a time, in the K loop, cost 5 us a tile.
+    Tile mine;
+    auto fill = [&](int batch) {
+        mine = Tile{0, 0, 0, 0};
+        const int64_t at = blockIdx.x + (int64_t)(batch * 64 + lane) * gridDim.x;
+        const bool have = at < ntiles;
         // each XCD (workgroup index modulo 8; the grid is a multiple of 8 or
         // the tiles are its first) takes a contiguous range
-        const int64_t q8 = ntiles >> 3, r8 = ntiles & 7, xcd = t & 7;
-        const int64_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (t >> 3);
+        const int t = have ? (int)at : 0, q8 = ntiles >> 3, r8 = ntiles & 7, xcd = t & 7;
+        const int tile = xcd * q8 + min(xcd, r8) + (t >> 3);
         if constexpr (GROUPED) {
-            MxRows x;
-            mx_find<BM, true>(a, tile, tiles_n, x);
-            // within an expert: groups of eight row tiles, row tiles fastest
-            const int in_e = (int)(tile - x.before * tiles_n);
-            const int per = 8 * tiles_n, grp = in_e / per, gm = min(x.cm - grp * 8, 8), in_g = in_e - grp * per;
-            const int m = grp * 8 + in_g % gm;
-            r.tn = in_g / gm;
-            r.e = x.e;
-            r.m0 = x.m0 + (int64_t)m * BM;
-            r.rows = min(x.rows - m * BM, BM);
+            mx_rows_of<BM>(a, tile, tiles_n, mine.e, mine.m0, mine.tn, mine.rows);
+            if (!have) mine.rows = 0;
         } else {
             // groups of four row tiles: an XCD's 32 concurrent tiles span 4 x 8 blocks
-            const int tl = (int)tile, per = 4 * tiles_n, grp = tl / per, gm = min(tiles_m - grp * 4, 4), in_g = tl - grp * per;
-            r.m0 = (int64_t)(grp * 4 + in_g % gm) * BM;
-            r.tn = in_g / gm;
-            r.rows = (int)min(a.M - r.m0, (int64_t)BM);
+            const int per = 4 * tiles_n, grp = tile / per, gm = min(tiles_m - grp * 4, 4), in_g = tile - grp * per;
+            mine.m0 = (grp * 4 + in_g % gm) * BM;
+            mine.tn = in_g / gm;
+            mine.rows = have ? (int)min(a.M - mine.m0, (int64_t)BM) : 0;
         }
-        return r;
+    };
+    auto tile_of = [&](int i) {
+        if (i && !(i & 63)) fill(i >> 6);
+        const int l = i & 63;
+        return Tile{__builtin_amdgcn_readlane(mine.m0, l), __builtin_amdgcn_readlane(mine.rows, l),
+                    __builtin_amdgcn_readlane(mine.tn, l), __builtin_amdgcn_readlane(mine.e, l)};
     };
 
     // ---- DMA: wave w moves rows [w BM/4, (w + 1) BM/4) of A and 64 weight columns
@@ -404,7 +457,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
         auto src_row = [&](int i) -> int64_t {
             if (i >= t.rows) return -1;
             if (!gather) return i;
-            const int64_t s = a.rows[t.m0 + i];
+            const int64_t s = a.rows[(int64_t)t.m0 + i];
             return s >= 0 && s < a.M ? s : -1;
         };
 #pragma unroll
@@ -419,8 +472,8 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             const int64_t s = r0 < BM ? src_row(r0 + (lane >> 1)) : -1;
             savo[i] = s < 0 ? kOut : (uint32_t)(s * 8 + (lane & 1) * 4);
         }
-        ra = mx_rsrc(gather ? a.a : a.a + t.m0 * pitch, kOut);
-        rsa = mx_rsrc(gather ? a.sa : a.sa + t.m0 * 8, kOut);
+        ra = mx_rsrc(mx_uniform(gather ? a.a : a.a + (int64_t)t.m0 * pitch), kOut);
+        rsa = mx_rsrc(mx_uniform(gather ? a.sa : a.sa + (int64_t)t.m0 * 8), kOut);
         // the wave's 64 weight columns (gated: even waves gates, odd waves ups)
         const int64_t col0 = GATED ? (int64_t)t.tn * 128 + (wave >> 1) * 64 : (int64_t)t.tn * 256 + wave * 64;
         const int64_t ncols = t.rows == 0 ? 0 : GATED ? F : N;
@@ -431,8 +484,8 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             bvo[i] = 8 * i + l8 < left ? (uint32_t)((8 * i + l8) * pitch + (ch ^ ((i & 2) * 2)) * 16) : kOut;
 #pragma unroll
         for (int i = 0; i < 2; ++i) sbvo[i] = 32 * i + (lane >> 1) < left ? lane * 4u + i * 256u : kOut;
-        rb = mx_rsrc(a.b + ((int64_t)t.e * N + wcol) * pitch, kOut);
-        rsb = mx_rsrc(a.sb + ((int64_t)t.e * nsteps * N + wcol) * 8, kOut);
+        rb = mx_rsrc(mx_uniform(a.b + ((int64_t)t.e * N + wcol) * pitch), kOut);
+        rsb = mx_rsrc(mx_uniform(a.sb + ((int64_t)t.e * nsteps * N + wcol) * 8), kOut);
     };
 
     // The DMA of one step, an instruction at a time: `Dma` holds what its
@@ -466,16 +519,15 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     };
     // The steps of all tiles form one sequence; the DMA runs two steps, so up
     // to two tiles, ahead of the MFMAs.
-    Tile cur = tile_of(blockIdx.x), q0{0, 0, 0, 0}, q1 = q0;
+    fill(0);
+    Tile cur = tile_of(0), q0{0, 0, 0, 0}, q1 = q0;
     if (cur.rows == 0) return;
-    int64_t t_dma = blockIdx.x;
-    int s_dma = 0, ahead = 0;
+    int t_dma = 0, s_dma = 0, ahead = 0;
     set_dma(cur);
     auto advance = [&]() {
         if (++s_dma < nsteps) return;
         s_dma = 0;
-        t_dma += gridDim.x;
-        const Tile t = tile_of(t_dma);
+        const Tile t = tile_of(++t_dma);
         set_dma(t);
         // (by value: a choice of addresses would put the queue in memory)
         auto put = [&](Tile& q, bool here) {
@@ -661,7 +713,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
                     }
                     const int row = row0 + 32 * mt;
                     if (row < cur.rows) {
-                        if (in_f) *(v2u*)(a.out_codes + ((cur.m0 + row) * F + f0) / 2) = (v2u){c[0], c[1]};
+                        if (in_f) *(v2u*)(a.out_codes + (((int64_t)cur.m0 + row) * F + f0) / 2) = (v2u){c[0], c[1]};
                         // one lane per block writes its scale; columns past F, up
                         // to the end of the slab (which a last tile may fill only
                         // half), get zeros
@@ -893,14 +945,60 @@ template <int MT> hipError_t launch_skinny(const Mx4GemmArgs& a, hipStream_t st)
 
 }  // namespace
 
+namespace {
+
+// Rows of a skinny pass, and 16-column tiles per wave
+int skinny_rows(const Mx4GemmArgs& a)
+{
+    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+// Estimated microseconds of each kernel.  Tiles: the 256 workgroups take them
+// in rounds; a step (256 k) of a 64, 128, 256 row tile measured 0.72, 0.99,
+// 1.46 us with all CUs busy, and a tile's beginning and end 3.2, 4.1, 8.1 us
+// (16384 x 2560 outputs at K = 3840 and 7680: 140.2 and 248.6, 94.7 and 168.8,
+// 89.9 and 155.5 us).  Skinny: 2.5 us, then weights at 5 TB/s and, for each
+// column group, the rows again at 6 TB/s (10240 x 10240 weights with 1, 16, 32,
+// 64 rows: 14.9, 18.3, 23.8, 34.6 us).  Groups of unknown size are taken to
+// fill half of their last tile.
+double tile_us(const Mx4GemmArgs& a, int bm, double step, double ends)
+{
+    const double tn = a.out_codes ? (double)((a.N / 2 + 127) / 128) : (double)((a.N + 255) / 256);
+    double tm = (double)((a.M + bm - 1) / bm);
+    if (a.E) {
+        const double groups = (double)(a.E < a.R ? a.E : a.R);
+        tm = (double)a.R / bm + 0.5 * groups;
+        if (tm < groups * 0.7) tm = groups * 0.7;
+    }
+    const double rounds = (double)(int64_t)((tm * tn + 255) / 256);
+    return rounds * ((double)((a.K + 255) / 256) * step + ends);
+}
+
+double skinny_us(const Mx4GemmArgs& a)
+{
+    const int rows = skinny_rows(a);
+    double passes = (double)((a.M + rows - 1) / rows);
+    if (a.E) {
+        const double groups = (double)(a.E < a.R ? a.E : a.R);
+        passes = (double)a.R / rows + 0.5 * groups;
+        if (passes < groups * 0.7) passes = groups * 0.7;
+    }
+    const double weights = (double)a.N * (double)a.K * 17 / 32 * 1e-6;   // MB
+    return 2.5 + passes * weights * (1 / 5.0 + (double)rows / (a.out_codes ? 64 : 32) / 6.0);
+}
+
+}  // namespace
+
 int mx4_gemm_path(const Mx4GemmArgs& a)
 {
-    // rows a weight tile meets: all of them, or an expert's share
-    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
-    if (rows <= 64) return kMx4Skinny;
-    if (rows <= 128) return kMx4Tile64;
-    if (rows <= 512) return kMx4Tile128;
-    return kMx4Tile256;
+    const double t[4] = {skinny_us(a), tile_us(a, 64, 0.72, 3.2), tile_us(a, 128, 0.99, 4.1), tile_us(a, 256, 1.46, 8.1)};
+    // (past 128 rows a weight column would be read three times and more)
+    const bool few = (a.E ? (a.R + a.E - 1) / a.E : a.M) <= 128;
+    int best = kMx4Tile64;
+    for (int i = kMx4Tile128; i <= kMx4Tile256; ++i)
+        if (t[i] < t[best]) best = i;
+    return few && t[kMx4Skinny] < t[best] ? kMx4Skinny : best;
 }
 
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t st)
@@ -910,8 +1008,8 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t st)
     case kMx4Tile128: return launch_tile<128>(a, st);
     case kMx4Tile64: return launch_tile<64>(a, st);
     }
-    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
-    return rows <= 16 ? launch_skinny<1>(a, st) : rows <= 32 ? launch_skinny<2>(a, st) : launch_skinny<4>(a, st);
+    const int rows = skinny_rows(a);
+    return rows == 16 ? launch_skinny<1>(a, st) : rows == 32 ? launch_skinny<2>(a, st) : launch_skinny<4>(a, st);
 }
 
 }  // namespace w4a4
