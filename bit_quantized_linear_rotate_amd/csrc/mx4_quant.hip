@@ -25,41 +25,41 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mq_rsrc(const void* base, uint
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)n, 0x00020000);
 }
 
-// the value of the lane whose index differs in bit D (D = 1, 2, 4, 8, 16)
+// the value of the lane whose index differs in bit D (D = 1, 2, 4, 8)
 template <int D> __device__ __forceinline__ uint32_t mq_xor(uint32_t v)
 {
     if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);        // quad [1,0,3,2]
     else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true);   // quad [2,3,0,1]
     else if constexpr (D == 4)                                                             // 7 - i, then quad [3,2,1,0]
         return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
-    else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, 0xf, 0xf, true);  // row rotate by 8
-    else return __builtin_amdgcn_ds_swizzle(v, 0x401f);                                    // xor 16
+    else return __builtin_amdgcn_mov_dpp(v, 0x128, 0xf, 0xf, true);                        // row rotate by 8
 }
 
-template <int D> __device__ __forceinline__ void butterfly_across(float (&v)[8], int lane)
+template <int D> __device__ __forceinline__ void butterfly_across(float (&v)[16], int lane)
 {
     const float s = (lane & D) ? -1.0f : 1.0f;   // upper partner: other - own, lower: own + other
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < 16; ++e)
         v[e] = __builtin_fmaf(s, v[e], __uint_as_float(mq_xor<D>(__float_as_uint(v[e]))));
 }
 
-template <int G> __device__ __forceinline__ void rotate8(float (&v)[8], int lane)
+// sixteen consecutive values per lane: distances 1, 2, 4, 8 within the lane,
+// 16, 32, 64, 128 across lanes
+template <int G> __device__ __forceinline__ void rotate16(float (&v)[16], int lane)
 {
 #pragma unroll
-    for (int d = 1; d < 8; d *= 2)
+    for (int d = 1; d < 16; d *= 2)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 16; ++e)
             if (!(e & d)) {
                 const float a = v[e], b = v[e + d];
                 v[e] = add_rn(a, b);
                 v[e + d] = add_rn(a, -b);
             }
-    if constexpr (G >= 16) butterfly_across<1>(v, lane);
-    if constexpr (G >= 32) butterfly_across<2>(v, lane);
-    if constexpr (G >= 64) butterfly_across<4>(v, lane);
-    if constexpr (G >= 128) butterfly_across<8>(v, lane);
-    if constexpr (G >= 256) butterfly_across<16>(v, lane);
+    if constexpr (G >= 32) butterfly_across<1>(v, lane);
+    if constexpr (G >= 64) butterfly_across<2>(v, lane);
+    if constexpr (G >= 128) butterfly_across<4>(v, lane);
+    if constexpr (G >= 256) butterfly_across<8>(v, lane);
 }
 
 template <int G> constexpr float inv_sqrt()
@@ -67,45 +67,76 @@ template <int G> constexpr float inv_sqrt()
     // fp32(1 / sqrt(g))
     return G == 16 ? 0.25f : G == 32 ? 0.17677669529663687f : G == 64 ? 0.125f : G == 128 ? 0.08838834764831845f : 0.0625f;
 }
+// g = 16, 64, 256: 1 / sqrt(g) = 2^-k, an exponent's worth; else 0
+template <int G> constexpr int inv_sqrt_exp() { return G == 16 ? 2 : G == 64 ? 3 : G == 256 ? 4 : 0; }
 
-// one byte of signs per element -> sign bits
-__device__ __forceinline__ uint32_t sign_of(const v2u s, int e)
+// the fp32 bits of the largest magnitude of sixteen values, NaN and infinity
+// on top
+template <int G> __device__ __forceinline__ uint32_t amax_bits(const float (&v)[16])
 {
-    return (e < 4 ? s[0] << (24 - 8 * e) : s[1] << (24 - 8 * (e - 4))) & 0x80000000u;
+    if constexpr (G >= 32) {
+        // A NaN or an infinity leaves nothing finite in its rotation group, so
+        // not in the block either: the float maximum, which passes over NaN
+        // beside numbers, sees it.
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) m = e ? fmaxf(fmaxf(m, fabsf(v[e])), fabsf(v[e + 1])) : fmaxf(fabsf(v[0]), fabsf(v[1]));
+        return __float_as_uint(m);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+    return m;
 }
 
-// A half wave holds 256 consecutive k of a row, eight per lane; a workgroup
-// takes U * 8 rows of one slab, so its scale bytes lie side by side, and every
-// lane has U rows in flight.  VEC: 16-byte loads from contiguous aligned rows;
-// else one load per element at any strides.
+// Sixteen lanes hold 256 consecutive k of a row, sixteen per lane (the more a
+// lane holds, the fewer butterflies cross lanes, and those cost twice); a
+// workgroup takes U * 16 rows of one slab, so its scale bytes lie side by side,
+// and every lane has U rows in flight.  VEC: 16-byte loads from contiguous
+// aligned rows; else one load per element at any strides.
 template <int DT, int G, bool VEC, int U>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4QuantArgs a)
 {
-    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15;
     const int64_t M = a.M, K = a.K;
     const int64_t slab = blockIdx.y;
-    const int64_t k0 = slab * kMxSlab + l32 * 8;
-    const int64_t row0 = (int64_t)blockIdx.x * (8 * U) + (tid >> 5);
+    const int64_t k0 = slab * kMxSlab + l16 * 16;
+    const int64_t row0 = (int64_t)blockIdx.x * (16 * U) + (tid >> 4);
     const bool in_k = k0 < K;
-    v2u si = {0, 0}, so = {0, 0};
+    constexpr int ESZ = DT == F32 ? 4 : 2, W = 4 * ESZ;   // 32-bit words of a lane's values
+    // input signs as sign bits of those words, output signs as those of codes
+    uint32_t si[W], so[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < W; ++i) si[i] = 0;
     if constexpr (G > 0) {
-        const int o = (l32 * 8) & (G - 1);
-        if (a.sign_in) si = (v2u){((const unsigned*)(a.sign_in + o))[0], ((const unsigned*)(a.sign_in + o))[1]};
-        if (a.sign_out) so = (v2u){((const unsigned*)(a.sign_out + o))[0], ((const unsigned*)(a.sign_out + o))[1]};
+        // (the sign bytes are 8-byte aligned)
+        const int o = (l16 * 16) & (G - 1);
+        auto negative = [&](const int8_t* s, int e) {
+            const v2u w = ((const v2u*)(s + o))[e >> 3];
+            return (w[(e >> 2) & 1] >> (8 * (e & 3) + 7)) & 1u;
+        };
+        if (a.sign_in)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if constexpr (DT == F32) si[e] = negative(a.sign_in, e) << 31;
+                else si[e >> 1] |= negative(a.sign_in, e) << (15 + 16 * (e & 1));
+            }
+        if (a.sign_out)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) so[e >> 3] |= negative(a.sign_out, e) << (3 + 4 * (e & 7));
     }
-    constexpr int ESZ = DT == F32 ? 4 : 2;
-    uint32_t raw[U][2 * ESZ];
+    uint32_t raw[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t row = row0 + 8 * u;
+        const int64_t row = row0 + 16 * u;
         const bool in = in_k && row < M;
 #pragma unroll
-        for (int i = 0; i < 2 * ESZ; ++i) raw[u][i] = 0;
+        for (int i = 0; i < W; ++i) raw[u][i] = 0;
         if constexpr (VEC) {
             if (in) {
                 const v4u* p = (const v4u*)((const char*)a.x + (row * a.sm + k0) * ESZ);
 #pragma unroll
-                for (int i = 0; i < ESZ / 2; ++i) {
+                for (int i = 0; i < ESZ; ++i) {
                     const v4u t = p[i];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) raw[u][4 * i + c] = t[c];
@@ -113,7 +144,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4QuantArgs a)
             }
         } else if (in) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 16; ++e) {
                 const int64_t at = row * a.sm + (k0 + e) * a.sk;
                 if constexpr (DT == F32) raw[u][e] = ((const uint32_t*)a.x)[at];
                 else raw[u][e >> 1] |= (uint32_t)((const uint16_t*)a.x)[at] << (16 * (e & 1));
@@ -122,39 +153,48 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4QuantArgs a)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t row = row0 + 8 * u;
-        float v[8];
+        const int64_t row = row0 + 16 * u;
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (DT == F32) v[e] = __uint_as_float(raw[u][e]);
-            else v[e] = h_to_f32<DT>((uint16_t)(raw[u][e >> 1] >> (16 * (e & 1))));
+        for (int e = 0; e < 16; ++e) {
+            if constexpr (DT == F32) v[e] = __uint_as_float(raw[u][e] ^ si[e]);
+            else v[e] = h_to_f32<DT>((uint16_t)((raw[u][e >> 1] ^ si[e >> 1]) >> (16 * (e & 1))));
         }
-        if constexpr (G > 0) {
+        if constexpr (G > 0) rotate16<G>(v, lane);
+        constexpr int KEXP = inv_sqrt_exp<G>();
+        if constexpr (G > 0 && KEXP == 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(__float_as_uint(v[e]) ^ sign_of(si, e));
-            rotate8<G>(v, lane);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = __uint_as_float(__float_as_uint(mul_rn(v[e], inv_sqrt<G>())) ^ sign_of(so, e));
+            for (int e = 0; e < 16; ++e) v[e] = mul_rn(v[e], inv_sqrt<G>());
         }
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+        uint32_t m = amax_bits<G>(v);
         m = max(m, mq_xor<1>(m));
-        m = max(m, mq_xor<2>(m));
-        const uint32_t ex = m >> 23;
+        int k = KEXP;   // y = v * 2^-k
+        if constexpr (KEXP > 0) {
+            // Near the subnormals the multiplication rounds, so it is done.
+            if (__any(m && m < (40u << 23))) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = mul_rn(v[e], inv_sqrt<G>());
+                m = amax_bits<G>(v);
+                m = max(m, mq_xor<1>(m));
+                k = 0;
+            }
+        }
+        const int ex = (int)(m >> 23);
         const bool bad = ex == 255;
-        const uint32_t byte = bad ? 255u : ex > 2 ? ex - 2 : 0u;
-        const float sc = __uint_as_float(byte << 23);   // the conversion reads the exponent field only
-        uint32_t c = 0;
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], sc, 1);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], sc, 2);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], sc, 3);
-        if (bad) c = 0;
+        const int byte = bad ? 255 : ex > 2 + k ? ex - 2 - k : 0;
+        const float sc = __uint_as_float((uint32_t)(byte + k) << 23);   // the conversion reads the exponent field only
+        uint32_t c[2] = {0, 0};
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 0], v[8 * p + 1], sc, 0);
+            c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 2], v[8 * p + 3], sc, 1);
+            c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 4], v[8 * p + 5], sc, 2);
+            c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 6], v[8 * p + 7], sc, 3);
+            c[p] = bad ? 0u : c[p] ^ so[p];
+        }
         if (row < M) {
-            if (in_k) *(uint32_t*)(a.codes + row * (K >> 1) + (k0 >> 1)) = c;
-            if (!(lane & 3)) a.scales[(slab * M + row) * 8 + (l32 >> 2)] = (uint8_t)(in_k ? byte : 0u);
+            if (in_k) *(v2u*)(a.codes + row * (K >> 1) + (k0 >> 1)) = (v2u){c[0], c[1]};
+            if (!(lane & 1)) a.scales[(slab * M + row) * 8 + (l16 >> 1)] = (uint8_t)(in_k ? byte : 0);
         }
     }
 }
@@ -196,14 +236,14 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t* __re
 
 template <int DT, int G, bool VEC> hipError_t quantize_u(const Mx4QuantArgs& a, hipStream_t st)
 {
-    // Four rows in flight per lane once that still leaves a workgroup for
+    // Two rows in flight per lane once that still leaves a workgroup for
     // every CU several times over; a decode batch spreads over the CUs instead.
     const unsigned slabs = (unsigned)mx4_slabs(a.K);
     if ((a.M + 31) / 32 * slabs >= 1024)
-        hipLaunchKernelGGL((mx4_quantize_kernel<DT, G, VEC, 4>), dim3((unsigned)((a.M + 31) / 32), slabs), dim3(256), 0,
+        hipLaunchKernelGGL((mx4_quantize_kernel<DT, G, VEC, 2>), dim3((unsigned)((a.M + 31) / 32), slabs), dim3(256), 0,
                            st, a);
     else
-        hipLaunchKernelGGL((mx4_quantize_kernel<DT, G, VEC, 1>), dim3((unsigned)((a.M + 7) / 8), slabs), dim3(256), 0,
+        hipLaunchKernelGGL((mx4_quantize_kernel<DT, G, VEC, 1>), dim3((unsigned)((a.M + 15) / 16), slabs), dim3(256), 0,
                            st, a);
     return hipGetLastError();
 }
