@@ -195,11 +195,12 @@ def _need(t, name: str, shape=None, dtypes=None, contiguous: bool = True):
 
 def _same_device(ref: torch.Tensor, **tensors):
     """Every tensor on the CUDA (HIP) device of `ref`."""
-    if ref.device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA (HIP) device, got {ref.device}")
+    device = ref.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA (HIP) device, got {device}")
     for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
@@ -1186,7 +1187,7 @@ def w4a4_linear_mx4(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tens
                                _ptr(w_scales), N, _ptr(bias), _ptr(out), _DT[out_dtype], _ptr(workspace),
                                workspace.numel(), _stream(dev))
     _check(rc, "w4a4_linear_mx4")
-    return out.view(*lead, N)
+    return out if len(lead) == 1 else out.view(*lead, N)
 
 
 # ---- products grouped by expert --------------------------------------------------
@@ -1334,4 +1335,4 @@ def w4a4_experts_mx4(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_code
         logits.stride(0), E, top_k, int(bool(renormalize)), _ptr(w13_codes), _ptr(w13_scales), F, _ptr(w2_codes),
         _ptr(w2_scales), _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev))
     _check(rc, "w4a4_experts_mx4")
-    return out.view(*lead, K)
+    return out if len(lead) == 1 else out.view(*lead, K)

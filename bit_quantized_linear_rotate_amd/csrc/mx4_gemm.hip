@@ -358,15 +358,15 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
 // BM x 256 outputs per workgroup of four waves (2 x 2, each BM/2 x 128), K in
 // steps of 256; one workgroup per CU, which takes tiles in turn.
 //   * A step's codes (128 bytes a row) and scales (8 bytes a row) go global ->
-//     LDS by DMA into one of two slots, two steps ahead of their use and, at a
-//     tile's end, into the next tile's steps.  16-byte chunk c of a row sits at
+//     LDS by DMA into one of two or three slots, as many steps ahead of their
+//     use and, at a tile's end, into the next tiles' steps.  16-byte chunk c of a row sits at
 //     c ^ swizzle(row): a ds_read_b128 serves sixteen lanes a cycle (lanes
 //     {0-3, 12-15} of one group of sixteen and {4-11} of its neighbour), and
 //     these then hit sixteen different 16-byte bank groups.
 //   * A step is four quarters (t).  While one quarter's MFMAs run from
 //     registers, the fragments of the next are read from LDS.  Before the last
 //     quarter the waves wait for the next step's DMA and meet: then nobody
-//     reads this step's slot any more, and the DMA two steps ahead goes out
+//     reads this step's slot any more, and the DMA furthest ahead goes out
 //     into it, half in this quarter and half in the next step's first.
 //     Reads, DMA and addresses are dealt out between the MFMAs, whose 32
 //     cycles each hide them.
@@ -385,10 +385,11 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     // DMA of waves that have no rows, so that all issue the same)
     constexpr int AB = BM * 128, BB = 256 * 128, SAB = BM * 8, SBB = 256 * 8;
     constexpr int SLOT = AB + BB + SAB + SBB + (BM == 64 ? 256 : 0);
+    constexpr int SLOTS = BM == 256 ? 2 : 3;  // what LDS holds
     constexpr int AI = BM / 32;               // A DMA instructions per wave (8 rows each)
     constexpr int SAI = BM == 256 ? 2 : 1;    // of A's scales (32 rows each)
     constexpr int DMAS = AI + 8 + SAI + 2;    // all of a step's, per wave
-    __shared__ __align__(16) uint8_t smem[2 * SLOT];
+    __shared__ __align__(16) uint8_t smem[SLOTS * SLOT];
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -517,10 +518,10 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             mx_dma<4>(rsb, smem + sl + AB + BB + SAB + (wave * 64 + i * 32) * 8, sbvo[i & 1], d.sob);
         }
     };
-    // The steps of all tiles form one sequence; the DMA runs two steps, so up
-    // to two tiles, ahead of the MFMAs.
+    // The steps of all tiles form one sequence; the DMA runs SLOTS steps, so up
+    // to as many tiles, ahead of the MFMAs.
     fill(0);
-    Tile cur = tile_of(0), q0{0, 0, 0, 0}, q1 = q0;
+    Tile cur = tile_of(0), q0{0, 0, 0, 0}, q1 = q0, q2 = q0;
     if (cur.rows == 0) return;
     int t_dma = 0, s_dma = 0, ahead = 0;
     set_dma(cur);
@@ -538,6 +539,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
         };
         put(q0, ahead == 0);
         put(q1, ahead == 1);
+        if constexpr (SLOTS == 3) put(q2, ahead == 2);
         ++ahead;
     };
 
@@ -577,15 +579,15 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     };
 
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < SLOTS; ++s) {
         Dma d;
         dma_chunks(d, s_dma);
         dma_offsets(d, s_dma);
 #pragma unroll
         for (int n = 0; n < DMAS; ++n) dma(d, s * SLOT, n);
-        if (s == 0) advance();
+        if (s + 1 < SLOTS) advance();
     }
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DMAS) : "memory");   // the first step has landed
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((SLOTS - 1) * DMAS) : "memory");   // the first step has landed
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -597,7 +599,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     const int c0 = wn * 128 + 16 * h;      // columns sixteen from c0 + 32 nt
     const bool wide = !GATED && mx_wide_stores(a);
     constexpr int D1 = DMAS / 2;           // DMA instructions of the last quarter; the others follow
-    int sl = 0, stores = 0;                // stores: whether the last epilogue's may be in flight
+    int sl = 0, stores = 0;                // stores: steps in which the last epilogue's may be in flight
     Dma d;
     for (;;) {
         v16f acc[MT][NT];
@@ -613,7 +615,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             __builtin_amdgcn_sched_barrier(0);
         }
         for (int s = 0;;) {
-            const int nx = SLOT - sl;
+            const int nx = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
 #pragma unroll
             for (int k = 0; k < NM; ++k) {
                 mx_mma<1>(acc[k / NT][k % NT], fb[1][k % NT], fa[1][k / NT], fsb[k % NT], fsa[k / NT]);
@@ -629,18 +631,21 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
                 if (k == NM * 3 / 4) dma_offsets(d, s_dma);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            // The next step has landed (in a tile's first step all but the
-            // stores of the tile before, which went out after it), and this
-            // one is read.
+            // The next step has landed, and this one is read.  Still in flight
+            // may be the DMA of the steps after the next and, in a tile's first
+            // SLOTS - 1 steps, the stores of the tile before, which went out
+            // after it.
             asm volatile("s_waitcnt lgkmcnt(0)\n\t"
-                         "s_cmp_eq_u32 %0, 0\n\t"
+                         "s_cmp_lt_i32 %0, 1\n\t"
                          "s_cbranch_scc1 1f\n\t"
                          "s_waitcnt vmcnt(%1)\n\t"
                          "s_branch 2f\n"
                          "1:\n\t"
-                         "s_waitcnt vmcnt(0)\n"
-                         "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"(8 * MT) : "memory", "scc");
-            stores = 0;
+                         "s_waitcnt vmcnt(%2)\n"
+                         "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"((SLOTS - 2) * DMAS + 8 * MT),
+                         "n"((SLOTS - 2) * DMAS)
+                         : "memory", "scc");
+            --stores;
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
@@ -666,7 +671,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
         }
 #pragma unroll
         for (int i = D1; i < DMAS; ++i) dma(d, sl, i);
-        sl = SLOT - sl;
+        sl = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) mx_settle(acc[mt]);
 
@@ -731,10 +736,11 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             if (a.out_dtype == BF16) mx_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
             else if (a.out_dtype == F16) mx_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
             else mx_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
-            stores = wide;
+            stores = wide ? SLOTS - 1 : 0;
         }
         cur = q0;
         q0 = q1;
+        if constexpr (SLOTS == 3) q1 = q2;
         --ahead;
         if (cur.rows == 0) break;
     }
@@ -955,13 +961,13 @@ int skinny_rows(const Mx4GemmArgs& a)
 }
 
 // Estimated microseconds of each kernel.  Tiles: the 256 workgroups take them
-// in rounds; a step (256 k) of a 64, 128, 256 row tile measured 0.72, 0.99,
-// 1.46 us with all CUs busy, and a tile's beginning and end 3.2, 4.1, 8.1 us
-// (16384 x 2560 outputs at K = 3840 and 7680: 140.2 and 248.6, 94.7 and 168.8,
-// 89.9 and 155.5 us).  Skinny: 2.5 us, then weights at 5 TB/s and, for each
-// column group, the rows again at 6 TB/s (10240 x 10240 weights with 1, 16, 32,
-// 64 rows: 14.9, 18.3, 23.8, 34.6 us).  Groups of unknown size are taken to
-// fill half of their last tile.
+// in rounds; a step (256 k) of a 64, 128, 256 row tile measured 0.66, 1.0,
+// 1.46 us with all CUs busy, and a tile's beginning and end 3.7, 4.2, 9.4 us
+// (16384 x 2560 outputs at K = 3840 and 7680: 136 and 235, 96 and 171, 95 and
+// 161 us).  Skinny: 2.5 us, then weights at 5 TB/s and, for each column group,
+// the rows again at 6 TB/s (10240 x 10240 weights with 1, 16, 32, 64 rows:
+// 14.9, 18.3, 23.8, 34.6 us).  Groups of unknown size are taken to fill half
+// of their last tile.
 double tile_us(const Mx4GemmArgs& a, int bm, double step, double ends)
 {
     const double tn = a.out_codes ? (double)((a.N / 2 + 127) / 128) : (double)((a.N + 255) / 256);
@@ -992,13 +998,17 @@ double skinny_us(const Mx4GemmArgs& a)
 
 int mx4_gemm_path(const Mx4GemmArgs& a)
 {
-    const double t[4] = {skinny_us(a), tile_us(a, 64, 0.72, 3.2), tile_us(a, 128, 0.99, 4.1), tile_us(a, 256, 1.46, 8.1)};
-    // (past 128 rows a weight column would be read three times and more)
-    const bool few = (a.E ? (a.R + a.E - 1) / a.E : a.M) <= 128;
+    const double t[4] = {skinny_us(a), tile_us(a, 64, 0.66, 3.7), tile_us(a, 128, 1.0, 4.2), tile_us(a, 256, 1.46, 9.4)};
+    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
+    // Tiles of 256 rows are two steps ahead in their weights, the others three:
+    // not enough where a group's weights serve a few tiles only (32 experts of
+    // 3840 x 2560: 8192 rows 96 us against 73 with 128, 32768 rows 203 : 212).
+    const int last = a.E && rows < 1024 ? kMx4Tile128 : kMx4Tile256;
     int best = kMx4Tile64;
-    for (int i = kMx4Tile128; i <= kMx4Tile256; ++i)
+    for (int i = kMx4Tile128; i <= last; ++i)
         if (t[i] < t[best]) best = i;
-    return few && t[kMx4Skinny] < t[best] ? kMx4Skinny : best;
+    // (past 128 rows a weight column would be read three times and more)
+    return rows <= 128 && t[kMx4Skinny] < t[best] ? kMx4Skinny : best;
 }
 
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t st)

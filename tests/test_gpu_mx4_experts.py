@@ -27,13 +27,14 @@ CASES = {
     "tile256": ([256, 2049, 0, 513, 1, 700], 1),
     "large": ([700, 1, 900, 333, 0, 513, 64], 5),
     "larger": ([2300, 0, 1, 2049, 513], 2),
+    "largest": ([2600, 1, 2049, 513], 2),
     "many experts": ([i % 3 for i in range(200)], 0),
     "nothing routed": ([0, 0, 0], 7),
 }
 
 
 @pytest.mark.parametrize("name", CASES)
-@pytest.mark.parametrize("K,N", [(512, 256), (288, 77), (288, 2304), (96, 2561)])
+@pytest.mark.parametrize("K,N", [(512, 256), (288, 77), (288, 2304), (96, 2561), (1056, 2304)])
 def test_grouped_gemm(name, K, N):
     need_gpu()
     counts, extra = CASES[name]
@@ -103,13 +104,15 @@ def check_gated(codes, scales, g, u, eg, eu):
 
 
 def test_cases_reach_every_kernel():
-    for gated, widths in ((False, (256, 77, 2304, 2561)), (True, (512, 192, 320, 2368))):
-        got = {w4.w4a4_gemm_mx4_plan(sum(c) + x, 288, n, len(c), gated) for c, x in CASES.values() for n in widths}
+    shapes = {False: ((512, 256), (288, 77), (288, 2304), (96, 2561), (1056, 2304)),
+              True: ((512, 512), (288, 192), (256, 320), (288, 2368), (1056, 2368))}
+    for gated, widths in shapes.items():
+        got = {w4.w4a4_gemm_mx4_plan(sum(c) + x, k, n, len(c), gated) for c, x in CASES.values() for k, n in widths}
         assert got == {"skinny", "tile64", "tile128", "tile256"}, (gated, got)
 
 
 @pytest.mark.parametrize("name", CASES)
-@pytest.mark.parametrize("K,F", [(512, 256), (288, 96), (256, 160), (288, 1184)])
+@pytest.mark.parametrize("K,F", [(512, 256), (288, 96), (256, 160), (288, 1184), (1056, 1184)])
 def test_grouped_gated(name, K, F):
     need_gpu()
     counts, extra = CASES[name]
