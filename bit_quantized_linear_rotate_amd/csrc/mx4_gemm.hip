@@ -223,10 +223,13 @@ __device__ __forceinline__ void mx_zero_rows(const Mx4GemmArgs& a, int64_t part,
     }
 }
 
-// silu(g) * u in fp32: g / (1 + exp(-g)) * u
+// silu(g) * u in fp32: g (1 / (1 + exp(-g))) u.  The reciprocal is the
+// hardware's (1 ulp; the result is rounded to four bits next): a rounded
+// division is ten instructions a value, 2 us a tile of 256 x 128 results.  Where
+// it falls below 2^-126 (g < -87) it is zero.
 __device__ __forceinline__ float mx_gated(float g, float u)
 {
-    return mul_rn(g / add_rn(1.0f, __expf(-g)), u);
+    return mul_rn(mul_rn(g, __builtin_amdgcn_rcpf(add_rn(1.0f, __expf(-g)))), u);
 }
 
 // The scale byte of a block whose largest magnitude has fp32 bits m (255:
@@ -300,23 +303,64 @@ __device__ __forceinline__ void mx_bias(const Mx4GemmArgs& a, int e, int64_t fir
 }
 
 // The epilogue of a wave: rows row0 + 32 mt of the tile, sixteen consecutive
-// columns from n0 + c0 + 32 nt in this lane.  Wide stores are range-checked buffer stores, so that every wave issues the same
-// number of them, 4 MT times two (fp32: four), whatever the tile holds.
-template <int ODT, int MT>
-__device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
-                                            int64_t n0, int c0, int e, bool wide)
+// columns from n0 + c0 + 32 nt in this lane.  Wide stores are range-checked
+// buffer stores, so that every wave issues the same number of them, 4 MT times
+// two (fp32: four), whatever the tile holds; without a branch between them: two
+// per 32 x 32 outputs, for bias and width, cost 0.5 us a tile of 256 rows, in
+// instructions to fetch.
+template <int ODT, int MT, bool BIAS>
+__device__ __forceinline__ void mx_wide_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
+                                                 int64_t n0, int c0, int e)
 {
-    constexpr int ESZ = ODT == F32 ? 4 : 2;
+    constexpr int ESZ = ODT == F32 ? 4 : 2, PIECE = 16 / ESZ, P = 16 / PIECE;
     const int64_t N = a.N;
     const __amdgpu_buffer_rsrc_t ro =
         mx_rsrc(mx_uniform((const uint8_t*)a.out + (m0 * N + n0) * ESZ), ((int64_t)rows * N - n0) * ESZ);
-    const uint32_t rstep = (uint32_t)(32 * N * ESZ);
+    const uint32_t rstep = (uint32_t)(32 * N * ESZ), off = (uint32_t)((row0 * N + c0) * ESZ);
+    const int left = (int)min(N - n0, (int64_t)256) - c0;   // columns of the matrix from this lane's first
+    float bv[4][16];
+    if constexpr (BIAS) mx_bias<4>(a, e, 0, N, n0 + c0, bv);
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        uint32_t at[P];   // (past the resource, and so with any mt rstep, where the column does not exist)
+#pragma unroll
+        for (int p = 0; p < P; ++p) at[p] = 32 * nt + PIECE * p < left ? off + (32 * nt + PIECE * p) * ESZ : kOut;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float v[16];
+            mx_here(acc[mt][nt]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = acc[mt][nt][i];
+            if constexpr (BIAS) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = add_rn(v[i], bv[nt][i]);
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                v4u w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (ODT == F32) w[i] = __float_as_uint(v[4 * p + i]);
+                    else w[i] = mx_pack2<ODT>(v[8 * p + 2 * i], v[8 * p + 2 * i + 1]);
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(w, ro, (int)(at[p] + mt * rstep), 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
+        }
+    }
+}
+
+// ... and a value at a time
+template <int ODT, int MT>
+__device__ __forceinline__ void mx_narrow_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
+                                                   int64_t n0, int c0, int e)
+{
+    const int64_t N = a.N;
     float bv[4][16];
     if (a.bias) mx_bias<4>(a, e, 0, N, n0 + c0, bv);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         const int64_t c = n0 + c0 + 32 * nt;
-        const uint32_t off = (uint32_t)((row0 * N + c0 + 32 * nt) * ESZ);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float v[16];
@@ -327,31 +371,24 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = add_rn(v[i], bv[nt][i]);
             }
-            if (wide) {
-                if constexpr (ODT == F32) {
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            (v4u){__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]),
-                                  __float_as_uint(v[4 * p + 3])},
-                            ro, (int)(c + 4 * p < N ? off + mt * rstep + 16 * p : kOut), 0, 0);
-                } else {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            (v4u){mx_pack2<ODT>(v[8 * p], v[8 * p + 1]), mx_pack2<ODT>(v[8 * p + 2], v[8 * p + 3]),
-                                  mx_pack2<ODT>(v[8 * p + 4], v[8 * p + 5]), mx_pack2<ODT>(v[8 * p + 6], v[8 * p + 7])},
-                            ro, (int)(c + 8 * p < N ? off + mt * rstep + 16 * p : kOut), 0, 0);
-                }
-            } else if (row0 + 32 * mt < rows) {
-                char* o = (char*)a.out + ((m0 + row0 + 32 * mt) * N + c) * ESZ;
+            if (row0 + 32 * mt < rows) {
+                char* o = (char*)a.out + ((m0 + row0 + 32 * mt) * N + c) * (ODT == F32 ? 4 : 2);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (c + i < N) store_any(ODT, o, i, v[i]);
             }
-            __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+}
+
+template <int ODT, int MT>
+__device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
+                                            int64_t n0, int c0, int e, bool wide)
+{
+    if (!wide) mx_narrow_epilogue<ODT, MT>(a, acc, m0, row0, rows, n0, c0, e);
+    else if (a.bias) mx_wide_epilogue<ODT, MT, true>(a, acc, m0, row0, rows, n0, c0, e);
+    else mx_wide_epilogue<ODT, MT, false>(a, acc, m0, row0, rows, n0, c0, e);
 }
 
 // ---- the tile kernel ---------------------------------------------------------
