@@ -252,14 +252,6 @@ template <int ODT> __device__ __forceinline__ uint32_t mx_pack2(float lo, float 
     }
 }
 
-// Whether a tile's outputs go out as 16-byte pieces: rows 16-byte aligned (a
-// piece is then all in or all out) and a tile's rows within 2^31 bytes.
-__device__ __forceinline__ bool mx_wide_stores(const Mx4GemmArgs& a)
-{
-    const int esz = a.out_dtype == F32 ? 4 : 2;
-    return (a.N * esz) % 16 == 0 && (uintptr_t)a.out % 16 == 0 && a.N * esz < ((int64_t)1 << 23);
-}
-
 // The biases of this lane, columns c + 32 nt .. + 15 of the n that start at
 // column `first` of expert e's row (zeros from n on).  Loaded all together and
 // waited for here: the compiler's own waits would reach into the K loop.
@@ -303,28 +295,31 @@ __device__ __forceinline__ void mx_bias(const Mx4GemmArgs& a, int e, int64_t fir
 }
 
 // The epilogue of a wave: rows row0 + 32 mt of the tile, sixteen consecutive
-// columns from n0 + c0 + 32 nt in this lane.  Wide stores are range-checked
-// buffer stores, so that every wave issues the same number of them, 4 MT times
-// two (fp32: four), whatever the tile holds; without a branch between them: two
-// per 32 x 32 outputs, for bias and width, cost 0.5 us a tile of 256 rows, in
-// instructions to fetch.
-template <int ODT, int MT, bool BIAS>
-__device__ __forceinline__ void mx_wide_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
-                                                 int64_t n0, int c0, int e)
+// columns from n0 + c0 + 32 nt in this lane, as pieces of 16 bytes (the columns
+// of a row need not be aligned to them).  Range-checked buffer stores, so that
+// every wave issues the same number of them, 4 MT times two (fp32: four),
+// whatever the tile holds; without a branch between them: two per 32 x 32
+// outputs cost 0.5 us a tile of 256 rows, in instructions to fetch.  CUT: the
+// piece that the matrix's last column cuts goes out a value at a time (all of a
+// row that way: 8192 x 3841 outputs, K = 3840: 162 us, so 93, of 3840: 74).
+template <int ODT, int MT, bool BIAS, bool CUT>
+__device__ __forceinline__ void mx_put(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows, int64_t n0,
+                                       int c0, int e)
 {
     constexpr int ESZ = ODT == F32 ? 4 : 2, PIECE = 16 / ESZ, P = 16 / PIECE;
     const int64_t N = a.N;
     const __amdgpu_buffer_rsrc_t ro =
         mx_rsrc(mx_uniform((const uint8_t*)a.out + (m0 * N + n0) * ESZ), ((int64_t)rows * N - n0) * ESZ);
     const uint32_t rstep = (uint32_t)(32 * N * ESZ), off = (uint32_t)((row0 * N + c0) * ESZ);
-    const int left = (int)min(N - n0, (int64_t)256) - c0;   // columns of the matrix from this lane's first
+    const int left = (int)min(N - n0, (int64_t)256) - c0;   // columns from this lane's first (c0 is a multiple of 16)
     float bv[4][16];
     if constexpr (BIAS) mx_bias<4>(a, e, 0, N, n0 + c0, bv);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-        uint32_t at[P];   // (past the resource, and so with any mt rstep, where the column does not exist)
+        uint32_t at[P];   // (past the resource, and so with any mt rstep, where the piece is not whole)
 #pragma unroll
-        for (int p = 0; p < P; ++p) at[p] = 32 * nt + PIECE * p < left ? off + (32 * nt + PIECE * p) * ESZ : kOut;
+        for (int p = 0; p < P; ++p)
+            at[p] = 32 * nt + PIECE * (p + 1) <= left ? off + (32 * nt + PIECE * p) * ESZ : kOut;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float v[16];
@@ -345,50 +340,32 @@ __device__ __forceinline__ void mx_wide_epilogue(const Mx4GemmArgs& a, v16f (&ac
                 }
                 __builtin_amdgcn_raw_buffer_store_b128(w, ro, (int)(at[p] + mt * rstep), 0, 0);
             }
+            if constexpr (CUT) {
+                const int from = left / PIECE * PIECE - 32 * nt, to = left - 32 * nt;   // of these sixteen columns
+                if (row0 + 32 * mt < rows && from >= 0 && from < 16) {
+                    char* o = (char*)a.out + ((m0 + row0 + 32 * mt) * N + n0 + c0 + 32 * nt) * ESZ;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i >= from && i < to) store_any(ODT, o, i, v[i]);
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
-        }
-    }
-}
-
-// ... and a value at a time
-template <int ODT, int MT>
-__device__ __forceinline__ void mx_narrow_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
-                                                   int64_t n0, int c0, int e)
-{
-    const int64_t N = a.N;
-    float bv[4][16];
-    if (a.bias) mx_bias<4>(a, e, 0, N, n0 + c0, bv);
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        const int64_t c = n0 + c0 + 32 * nt;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float v[16];
-            mx_here(acc[mt][nt]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = acc[mt][nt][i];
-            if (a.bias) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = add_rn(v[i], bv[nt][i]);
-            }
-            if (row0 + 32 * mt < rows) {
-                char* o = (char*)a.out + ((m0 + row0 + 32 * mt) * N + c) * (ODT == F32 ? 4 : 2);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < N) store_any(ODT, o, i, v[i]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
 template <int ODT, int MT>
 __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows,
-                                            int64_t n0, int c0, int e, bool wide)
+                                            int64_t n0, int c0, int e)
 {
-    if (!wide) mx_narrow_epilogue<ODT, MT>(a, acc, m0, row0, rows, n0, c0, e);
-    else if (a.bias) mx_wide_epilogue<ODT, MT, true>(a, acc, m0, row0, rows, n0, c0, e);
-    else mx_wide_epilogue<ODT, MT, false>(a, acc, m0, row0, rows, n0, c0, e);
+    const bool cut = a.N - n0 < 256 && a.N % (ODT == F32 ? 4 : 8);
+    if (a.bias) {
+        if (cut) mx_put<ODT, MT, true, true>(a, acc, m0, row0, rows, n0, c0, e);
+        else mx_put<ODT, MT, true, false>(a, acc, m0, row0, rows, n0, c0, e);
+    } else {
+        if (cut) mx_put<ODT, MT, false, true>(a, acc, m0, row0, rows, n0, c0, e);
+        else mx_put<ODT, MT, false, false>(a, acc, m0, row0, rows, n0, c0, e);
+    }
 }
 
 // ---- the tile kernel ---------------------------------------------------------
@@ -634,7 +611,6 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     }
     const int row0 = wm * (BM / 2) + j;    // this lane's row (+ 32 mt), and of the
     const int c0 = wn * 128 + 16 * h;      // columns sixteen from c0 + 32 nt
-    const bool wide = !GATED && mx_wide_stores(a);
     constexpr int D1 = DMAS / 2;           // DMA instructions of the last quarter; the others follow
     int sl = 0, stores = 0;                // stores: steps in which the last epilogue's may be in flight
     Dma d;
@@ -770,10 +746,10 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
             }
         } else {
             const int64_t n0 = (int64_t)cur.tn * 256;
-            if (a.out_dtype == BF16) mx_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
-            else if (a.out_dtype == F16) mx_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
-            else mx_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e, wide);
-            stores = wide ? SLOTS - 1 : 0;
+            if (a.out_dtype == BF16) mx_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+            else if (a.out_dtype == F16) mx_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+            else mx_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+            stores = SLOTS - 1;
         }
         cur = q0;
         q0 = q1;
@@ -1044,6 +1020,9 @@ int mx4_gemm_path(const Mx4GemmArgs& a)
     int best = kMx4Tile64;
     for (int i = kMx4Tile128; i <= last; ++i)
         if (t[i] < t[best]) best = i;
+    // A tile's outputs are addressed with 31 bits: rows of 8 MB and more are the
+    // skinny kernel's.
+    if (!a.out_codes && a.N * (a.out_dtype == F32 ? 4 : 2) >= (int64_t)1 << 23) return kMx4Skinny;
     // (past 128 rows a weight column would be read three times and more)
     return rows <= 128 && t[kMx4Skinny] < t[best] ? kMx4Skinny : best;
 }
