@@ -1128,7 +1128,7 @@ def mx4_scales_to_rows(scales: torch.Tensor, K: int) -> torch.Tensor:
 
 
 def w4a4_gemm_mx4_plan(rows: int, K: int, N: int, experts: int = 0, gated: bool = False) -> str:
-    """Name of the kernel an MX4 product of `rows` rows takes (experts = 0: dense)."""
+    """Name of the kernel an MX4 product of `rows` rows takes (experts = 0: dense; 16-bit outputs)."""
     k = ctypes.c_int(-1)
     _check(lib().w4a4_gemm_mx4_plan(rows, K, N, experts, int(gated), ctypes.byref(k)), "w4a4_gemm_mx4_plan")
     return MX4_KERNELS.get(k.value, "none")

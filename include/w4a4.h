@@ -363,7 +363,8 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
  *   (N % 64 == 0); the result is the MX4 form of silu(gate) * up, taken from
  *   the fp32 sums: out_codes (R, N/4), out_scales (slabs of N/2, R, 8).
  * w4a4_gemm_mx4_plan (host-only): the kernel these calls take for `rows` rows
- *   (E = 0: dense): 0 skinny, 1 / 2 / 3 tiles of 64 / 128 / 256 rows, -1 none.
+ *   (E = 0: dense; 16-bit outputs): 0 skinny, 1 / 2 / 3 tiles of 64 / 128 /
+ *   256 rows, -1 none.
  * w4a4_route_experts: per token (row of logits, `stride` elements apart) the
  *   top_k experts by logit, equal logits by the lower index; NaN and -inf
  *   logits are never taken, so a token can have fewer than top_k (expert -1,

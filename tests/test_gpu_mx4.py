@@ -170,8 +170,8 @@ def test_gemm(M, K, N, out):
 def test_gemm_plans_cover_the_shapes():
     names = {w4.w4a4_gemm_mx4_plan(M, K, N) for M, K, N in SHAPES}
     assert names == {"skinny", "tile64", "tile128", "tile256"}
-    # rows of outputs that a tile's 31-bit offsets do not reach across
-    assert w4.w4a4_gemm_mx4_plan(1000, 64, 1 << 21) == "skinny" != w4.w4a4_gemm_mx4_plan(1000, 64, (1 << 21) - 256)
+    # 16-bit outputs whose rows a tile's 31-bit offsets do not reach across
+    assert w4.w4a4_gemm_mx4_plan(1000, 64, 1 << 22) == "skinny" != w4.w4a4_gemm_mx4_plan(1000, 64, (1 << 22) - 256)
 
 
 def test_gemm_nan_scales_reach_their_outputs_only():
