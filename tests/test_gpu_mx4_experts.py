@@ -1,5 +1,8 @@
 """GPU tests of the products grouped by expert, routing, combining and the expert
 layer, against plain forms in 64 bits (tests/mx4.py)."""
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -249,3 +252,16 @@ def test_experts_workspace_output_and_empty():
         got = w4.w4a4_experts_mx4(x, l, k, w13, s13, w2, s2)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, ref)
+
+
+def test_example_block():
+    """The example's block against single precision.  A value rounded to e2m1 under a
+    power-of-two scale is off by 0.1 to 0.13 of itself (rms), so a product of two rounded
+    operands by up to 0.19, gated products and the second product, whose operands carry that
+    too, by up to 0.33; the block is a sum of both kinds."""
+    need_gpu()
+    spec = importlib.util.spec_from_file_location("mx4_expert_block", os.path.join(
+        os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mx4_expert_block.py"))
+    block = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(block)
+    assert 0.05 < block.main(tokens=200, K=512, F=256, E=8, top_k=2, repeat=2) < 0.33
