@@ -2,11 +2,17 @@
 //
 // Routing.  Per token, k rounds of "largest logit, lowest index" over the E
 // logits by sixteen lanes (64 for many experts or choices); weights are
-// exp(l - max) over their sum (over the chosen or over all experts).  The (token, choice) slots are then sorted
-// by expert with a stable counting sort, so the order is a function of the
-// logits alone: chunks of tokens count their slots per expert, and every chunk
-// adds up the counts before it to place its own.  Counts are integers: the
-// order in which they are added does not matter.
+// exp(l - max) over their sum (over the chosen or over all experts).  The
+// (token, choice) slots are then sorted by expert with a stable counting sort,
+// so the order is a function of the logits alone: chunks of tokens count their
+// slots per expert, and every chunk adds up the counts before it to place its
+// own.  Counts are integers: the order in which they are added does not matter.
+//
+// Bounds.  A few megabytes: the k dependent rounds of a maximum over lanes, and
+// the launches.  One chunk (up to 64 tokens) is one launch, more are two, since
+// the sort needs all chunks' counts.  Measured: 32 tokens of 32 experts, 4
+// choices 3.8 us; 8192 of 128, 8 choices 8.7 + 6.4 us; 8192 of 32, 4 choices
+// 4.9 + 6.6 us.
 #include "common.hpp"
 #include "mx4.hpp"
 
@@ -249,7 +255,14 @@ template <int DT> hipError_t route_dt(const RouteArgs& a, hipStream_t st)
     return a.E <= 256 ? route_nv<DT, 64, 4>(a, st) : route_nv<DT, 64, 16>(a, st);
 }
 
-// Combining: 8 (fp32: 4) columns per thread, one token per workgroup row.
+// Combining: out[t] = sum_j w[t][j] y[pos[t][j]] in fp32, j in order, rounded
+// once.  8 (fp32: 4) columns per thread, one token per workgroup row.  Bound by
+// memory, y being read once: 8192 tokens of 4 rows of 3840 bf16 (315 MB) 58.6
+// us = 5.4 TB/s, a copy's rate.
+// (In the expert layer y is in the layer's 16-bit type, a second rounding next
+// to the output's: 2^-9 of a value, where its four-bit operands are 2^-4 off;
+// in fp32 the layer's largest array would be twice as large: 504 MB more to move,
+// 100 us on 430, at 8192 tokens.)
 template <int DT, bool VEC> __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a)
 {
     constexpr int V = VEC ? (DT == F32 ? 4 : 8) : 1;

@@ -391,6 +391,18 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
 //     them, so gate, up and the block of 32 results (two lane halves) meet in
 //     registers: silu, product, block scale and codes are the epilogue, and
 //     the 2 x 16-bit intermediate is never written.
+// Bounds (sizes are rows x K x columns).  8192 x 8192 x 8192 246 us = 4.5
+// PFLOP/s: the steps of 256-row tiles run at 5.8, the matrix core's rate with
+// random codes (the card is then at its power limit; zeros go at 9.6), the rest
+// is a tile's end, whose outputs leave in a burst of all CUs.  8192 x 10240 x
+// 3840 153 us; 8192 x 3840 x 3840 68 us: 55 without the epilogue, 6 for its
+// conversion, 8 for its stores.  Tiles of 128 and 64 rows read more LDS per MFMA
+// (a row's step goes at 0.73 and 0.55 of the rate) and are for outputs too few
+// to fill the CUs with larger ones: 16396 rows of 32 experts x 3840 x 2560 127
+// us; 333 x 5376 x 7168 20 us, 126 tiles for 256 CUs.  Gated: 32768 x 3840 x 2560
+// 189 us.
+// Storing a tile's outputs between the next tile's MFMAs, with two sets of
+// accumulators, was slower: the compiler moves them between registers.
 template <int BM, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int tiles_m, int tiles_n)
 {
@@ -765,6 +777,9 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 // steps of one group of 16 NT columns (gated, NT = 4: 32 gates and their 32
 // ups, one block of results); 8 / KW groups lie side by side.  The waves'
 // partial sums meet in LDS and are added in wave order.
+// Bound by the weights' bytes and, up to a few megabytes of them, by latency:
+// 3840 x 3840 weights (7.8 MB) with one row 4.1 us, 10240 x 10240 (56 MB) 14.9
+// us = 3.7 TB/s; 64 rows 34.6 us, each column group reading the rows again.
 constexpr int kSkinnyWaves = 8;
 template <int MT, int NT, int KW, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)

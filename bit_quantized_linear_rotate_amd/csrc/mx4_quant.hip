@@ -9,6 +9,16 @@
 // codes = e2m1(y / 2^X) to nearest, ties to the even code, saturated at 6.  y
 // stays in fp32 until the codes are taken: there is no rounding in between.
 // A block that holds a NaN or an infinity gets scale byte 255 and codes 0.
+//
+// Bounds.  x is read once and 17/32 of a byte written per value: memory, until
+// g = 128; from there the butterflies and the conversion.  A lane holds sixteen
+// consecutive values, sixteen lanes a slab of 256 of a row: butterflies up to
+// distance 8 are in registers, the others DPP moves within a row of sixteen
+// lanes, a block is two lanes and its scales and codes leave in whole words.
+// Measured (hot and cold differ by a tenth): 8192 x 3840 bf16, g = 64 16.9 us =
+// 4.7 TB/s (a copy of as many bytes 15.3), unrotated 13.4; 8192 x 10240 fp16,
+// g = 256 47 to 51 us = 4.2 TB/s; the way back 14.2 us = 5.6 TB/s; 32 x 3840
+// 3.2 and 2.6 us, a launch.
 #include "common.hpp"
 #include "mx4.hpp"
 
