@@ -368,6 +368,69 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
     }
 }
 
+// The gated epilogue of a wave: rows row0 + 32 mt of the tile, results 16 h +
+// 32 nt .. + 15 of the wave's 64 (columns tn 128 + wn 64 + ...) in this lane:
+// gates in accumulator nt, ups in 2 + nt.  Range-checked stores as above: two of
+// codes and one of the two blocks' scale bytes per row tile.  On the last tile,
+// which may fill half of its slab only, the other half's bytes become zeros.
+template <int MT, bool BIAS>
+__device__ __forceinline__ void mx_put_gated(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows, int tn,
+                                             bool last, int wn, int h, int e)
+{
+    const int64_t F = a.N >> 1, R = a.E ? a.R : a.M;
+    const int pitch = (int)(F >> 1);
+    const __amdgpu_buffer_rsrc_t rc = mx_rsrc(mx_uniform(a.out_codes + m0 * pitch), (int64_t)rows * pitch);
+    const __amdgpu_buffer_rsrc_t rs = mx_rsrc(mx_uniform(a.out_scales + ((int64_t)(tn >> 1) * R + m0) * 8), rows * 8);
+    const int64_t fw = (int64_t)tn * 128 + wn * 64 + 16 * h;
+    const bool in_f[2] = {fw < F, fw + 32 < F};   // F is a multiple of 32, so are the blocks
+    float bg[2][16], bu[2][16];
+    if constexpr (BIAS) {
+        mx_bias<2>(a, e, 0, F, fw, bg);
+        mx_bias<2>(a, e, F, F, fw, bu);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const uint32_t row = row0 + 32 * mt, at = row * pitch + (uint32_t)(fw >> 1);
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            float v[16];
+            uint32_t m = 0;
+            mx_here(acc[mt][nt]);
+            mx_here(acc[mt][2 + nt]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float g = acc[mt][nt][i], u = acc[mt][2 + nt][i];
+                if constexpr (BIAS) {
+                    g = add_rn(g, bg[nt][i]);
+                    u = add_rn(u, bu[nt][i]);
+                }
+                v[i] = mx_gated(g, u);
+                m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+            }
+            // the block's other sixteen: the two halves of the wave exchanged
+            const auto both = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+            const uint32_t byte = mx_scale_byte(max(both[0], both[1]));
+            const float sc = __uint_as_float(byte << 23);
+            uint32_t c[2] = {0, 0};
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 0], v[8 * p + 1], sc, 0);
+                c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 2], v[8 * p + 3], sc, 1);
+                c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 4], v[8 * p + 5], sc, 2);
+                c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 6], v[8 * p + 7], sc, 3);
+                if (byte == 255) c[p] = 0;
+            }
+            __builtin_amdgcn_raw_buffer_store_b64((v2u){c[0], c[1]}, rc, (int)(in_f[nt] ? at + 16 * nt : kOut), 0, 0);
+            bytes |= (in_f[nt] ? byte : 0u) << (8 * nt);
+            __builtin_amdgcn_sched_barrier(0);   // one block's values at a time
+        }
+        const int so = h == 0 ? (int)(row * 8 + (tn & 1) * 4 + wn * 2) : (int)kOut;
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bytes, rs, so, 0, 0);
+        if (last && !(tn & 1)) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)0, rs, so | 4, 0, 0);
+    }
+}
+
 // ---- the tile kernel ---------------------------------------------------------
 // BM x 256 outputs per workgroup of four waves (2 x 2, each BM/2 x 128), K in
 // steps of 256; one workgroup per CU, which takes tiles in turn.
@@ -400,7 +463,7 @@ __device__ __forceinline__ void mx_epilogue(const Mx4GemmArgs& a, v16f (&acc)[MT
 // (a row's step goes at 0.73 and 0.55 of the rate) and are for outputs too few
 // to fill the CUs with larger ones: 16396 rows of 32 experts x 3840 x 2560 127
 // us; 333 x 5376 x 7168 20 us, 126 tiles for 256 CUs.  Gated: 32768 x 3840 x 2560
-// 189 us.
+// 181 us.
 // Storing a tile's outputs between the next tile's MFMAs, with two sets of
 // accumulators, was slower: the compiler moves them between registers.
 template <int BM, bool GROUPED, bool GATED>
@@ -415,6 +478,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     constexpr int AI = BM / 32;               // A DMA instructions per wave (8 rows each)
     constexpr int SAI = BM == 256 ? 2 : 1;    // of A's scales (32 rows each)
     constexpr int DMAS = AI + 8 + SAI + 2;    // all of a step's, per wave
+    constexpr int PUTS = GATED ? 3 * MT : 8 * MT;   // stores of an epilogue, at least
     __shared__ __align__(16) uint8_t smem[SLOTS * SLOT];
 
     const int tid = threadIdx.x;
@@ -667,7 +731,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
                          "s_branch 2f\n"
                          "1:\n\t"
                          "s_waitcnt vmcnt(%2)\n"
-                         "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"((SLOTS - 2) * DMAS + 8 * MT),
+                         "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"((SLOTS - 2) * DMAS + PUTS),
                          "n"((SLOTS - 2) * DMAS)
                          : "memory", "scc");
             --stores;
@@ -702,67 +766,16 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 
         // ---- epilogue
         if constexpr (GATED) {
-            const int64_t R = GROUPED ? a.R : a.M;
-            const int64_t fw = (int64_t)cur.tn * 128 + wn * 64 + 16 * h;
-            float bg[2][16], bu[2][16];
-            if (a.bias) {
-                mx_bias<2>(a, cur.e, 0, F, fw, bg);
-                mx_bias<2>(a, cur.e, F, F, fw, bu);
-            }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const int64_t f0 = fw + 32 * nt;
-                const bool in_f = f0 < F;     // F is a multiple of 32, so are the blocks
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float v[16];
-                    uint32_t m = 0;
-                    mx_here(acc[mt][nt]);
-                    mx_here(acc[mt][2 + nt]);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float g = acc[mt][nt][i], u = acc[mt][2 + nt][i];
-                        if (a.bias) {
-                            g = add_rn(g, bg[nt][i]);
-                            u = add_rn(u, bu[nt][i]);
-                        }
-                        v[i] = mx_gated(g, u);
-                        m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-                    }
-                    m = max(m, (uint32_t)__shfl_xor((int)m, 32));   // the block's other sixteen
-                    const uint32_t byte = mx_scale_byte(m);
-                    const float sc = __uint_as_float(byte << 23);
-                    uint32_t c[2] = {0, 0};
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 0], v[8 * p + 1], sc, 0);
-                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 2], v[8 * p + 3], sc, 1);
-                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 4], v[8 * p + 5], sc, 2);
-                        c[p] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[p], v[8 * p + 6], v[8 * p + 7], sc, 3);
-                        if (byte == 255) c[p] = 0;
-                    }
-                    const int row = row0 + 32 * mt;
-                    if (row < cur.rows) {
-                        if (in_f) *(v2u*)(a.out_codes + (((int64_t)cur.m0 + row) * F + f0) / 2) = (v2u){c[0], c[1]};
-                        // one lane per block writes its scale; columns past F, up
-                        // to the end of the slab (which a last tile may fill only
-                        // half), get zeros
-                        if (h == 0) {
-                            uint8_t* o = a.out_scales + ((f0 >> 8) * R + cur.m0 + row) * 8 + ((f0 >> 5) & 7);
-                            o[0] = (uint8_t)(in_f ? byte : 0u);
-                            if (cur.tn == tiles_n - 1 && !(cur.tn & 1)) o[4] = 0;
-                        }
-                    }
-                    __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
-                }
-            }
+            const bool last = cur.tn == tiles_n - 1;
+            if (a.bias) mx_put_gated<MT, true>(a, acc, cur.m0, row0, cur.rows, cur.tn, last, wn, h, cur.e);
+            else mx_put_gated<MT, false>(a, acc, cur.m0, row0, cur.rows, cur.tn, last, wn, h, cur.e);
         } else {
             const int64_t n0 = (int64_t)cur.tn * 256;
             if (a.out_dtype == BF16) mx_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else if (a.out_dtype == F16) mx_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else mx_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
-            stores = SLOTS - 1;
         }
+        stores = SLOTS - 1;
         cur = q0;
         q0 = q1;
         if constexpr (SLOTS == 3) q1 = q2;
@@ -1037,7 +1050,7 @@ int mx4_gemm_path(const Mx4GemmArgs& a)
         if (t[i] < t[best]) best = i;
     // A tile's outputs are addressed with 31 bits: rows of 8 MB and more are the
     // skinny kernel's.
-    if (!a.out_codes && a.N * (a.out_dtype == F32 ? 4 : 2) >= (int64_t)1 << 23) return kMx4Skinny;
+    if (a.N * (a.out_codes ? 1 : a.out_dtype == F32 ? 4 : 2) >= (int64_t)1 << 23) return kMx4Skinny;
     // (past 128 rows a weight column would be read three times and more)
     return rows <= 128 && t[kMx4Skinny] < t[best] ? kMx4Skinny : best;
 }
