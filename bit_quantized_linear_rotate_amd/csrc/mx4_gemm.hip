@@ -792,7 +792,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 // partial sums meet in LDS and are added in wave order.
 // Bound by the weights' bytes and, up to a few megabytes of them, by latency:
 // 3840 x 3840 weights (7.8 MB) with one row 4.1 us, 10240 x 10240 (56 MB) 14.9
-// us = 3.7 TB/s; 64 rows 34.6 us, each column group reading the rows again.
+// us = 3.7 TB/s; 64 rows 27.4 us, each column group reading the rows again.
 constexpr int kSkinnyWaves = 8;
 template <int MT, int NT, int KW, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
@@ -964,14 +964,29 @@ template <int BM> hipError_t launch_tile(const Mx4GemmArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int MT, int NT, int KW, bool GATED> hipError_t launch_skinny_w(const Mx4GemmArgs& a, hipStream_t st)
+int skinny_rows(const Mx4GemmArgs& a)
+{
+    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+// 64 columns a group: a single pass of more than 16 rows whose groups of 32
+// would be more than the CUs; the rows are read half as often (10240 x 10240
+// weights, 32 and 64 rows: 19.9 and 27.4 us against 23.8 and 34.5; with several
+// passes or shorter K nothing or a loss: 128 rows 51.6 : 49.1, K = 1280 64 rows
+// 13.5 : 10.5).
+bool skinny_wide(const Mx4GemmArgs& a) { return !a.E && a.M > 16 && a.M <= 64 && a.K > 1792 && a.N > 32 * 256; }
+
+template <int MT, int NT, int KW, bool GATED, bool GROUPED = true> hipError_t launch_skinny_w(const Mx4GemmArgs& a, hipStream_t st)
 {
     constexpr int COLS = (GATED ? 32 : 16 * NT) * (kSkinnyWaves / KW);
     const int64_t n = GATED ? a.N / 2 : a.N;
     const unsigned tn = (unsigned)((n + COLS - 1) / COLS);
-    if (a.E) {
-        const unsigned tm = (unsigned)(a.R / (16 * MT) + (a.E < a.R ? a.E : a.R) + 1);
-        hipLaunchKernelGGL((mx4_skinny_kernel<MT, NT, KW, true, GATED>), dim3(tn, tm), dim3(512), 0, st, a);
+    if (GROUPED && a.E) {
+        if constexpr (GROUPED) {
+            const unsigned tm = (unsigned)(a.R / (16 * MT) + (a.E < a.R ? a.E : a.R) + 1);
+            hipLaunchKernelGGL((mx4_skinny_kernel<MT, NT, KW, true, GATED>), dim3(tn, tm), dim3(512), 0, st, a);
+        }
     } else if constexpr (!GATED) {
         hipLaunchKernelGGL((mx4_skinny_kernel<MT, NT, KW, false, false>), dim3(tn, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
                            dim3(512), 0, st, a);
@@ -985,6 +1000,8 @@ template <int MT> hipError_t launch_skinny(const Mx4GemmArgs& a, hipStream_t st)
     const bool deep = a.K > 1792;
     if (a.out_codes) return deep ? launch_skinny_w<MT, 4, 8, true>(a, st) : launch_skinny_w<MT, 4, 4, true>(a, st);
     // 32 columns a group once 16 would make more workgroups than the CUs hold
+    if constexpr (MT > 1)
+        if (skinny_wide(a)) return launch_skinny_w<MT, 4, 8, false, false>(a, st);
     const bool narrow = !a.E && (a.N + 15) / 16 * ((a.M + 16 * MT - 1) / (16 * MT)) <= 512;
     if (narrow) return deep ? launch_skinny_w<MT, 1, 8, false>(a, st) : launch_skinny_w<MT, 1, 4, false>(a, st);
     return deep ? launch_skinny_w<MT, 2, 8, false>(a, st) : launch_skinny_w<MT, 2, 4, false>(a, st);
@@ -995,19 +1012,13 @@ template <int MT> hipError_t launch_skinny(const Mx4GemmArgs& a, hipStream_t st)
 namespace {
 
 // Rows of a skinny pass, and 16-column tiles per wave
-int skinny_rows(const Mx4GemmArgs& a)
-{
-    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
-
 // Estimated microseconds of each kernel.  Tiles: the 256 workgroups take them
 // in rounds; a step (256 k) of a 64, 128, 256 row tile measured 0.66, 1.0,
 // 1.46 us with all CUs busy, and a tile's beginning and end 3.7, 4.2, 9.4 us
 // (16384 x 2560 outputs at K = 3840 and 7680: 136 and 235, 96 and 171, 95 and
 // 161 us).  Skinny: 2.5 us, then weights at 5 TB/s and, for each column group,
 // the rows again at 6 TB/s (10240 x 10240 weights with 1, 16, 32, 64 rows:
-// 14.9, 18.3, 23.8, 34.6 us).  Groups of unknown size are taken to fill half
+// 14.9, 18.3, 19.9, 27.4 us).  Groups of unknown size are taken to fill half
 // of their last tile.
 double tile_us(const Mx4GemmArgs& a, int bm, double step, double ends)
 {
@@ -1032,7 +1043,7 @@ double skinny_us(const Mx4GemmArgs& a)
         if (passes < groups * 0.7) passes = groups * 0.7;
     }
     const double weights = (double)a.N * (double)a.K * 17 / 32 * 1e-6;   // MB
-    return 2.5 + passes * weights * (1 / 5.0 + (double)rows / (a.out_codes ? 64 : 32) / 6.0);
+    return 2.5 + passes * weights * (1 / 5.0 + (double)rows / (a.out_codes || skinny_wide(a) ? 64 : 32) / 6.0);
 }
 
 }  // namespace

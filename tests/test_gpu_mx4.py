@@ -149,7 +149,7 @@ def operand(rows, K, seed, lead=()):
 SHAPES = [(1, 32, 1), (1, 3840, 96), (5, 288, 33), (16, 256, 16), (17, 512, 40), (33, 1056, 257), (64, 96, 300),
           (65, 512, 256), (100, 800, 129), (128, 3840, 260), (129, 256, 512), (300, 1312, 513), (512, 64, 24),
           (513, 512, 256), (700, 1056, 1000), (1030, 288, 77), (2100, 96, 2560), (2100, 32, 2561), (3900, 288, 2300),
-          (3900, 96, 2303)]
+          (3900, 96, 2303), (20, 1824, 8200), (50, 1824, 8259)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
