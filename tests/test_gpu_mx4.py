@@ -270,3 +270,15 @@ def test_offsets_past_32_bits():
     assert bool((out[2:524_287] == 0).all()) and bool((out[524_290:599_999] == 0).all())
     back = w4.w4a4_dequantize_mx4(codes, scales)
     assert torch.equal(back[rows], w4.w4a4_dequantize_mx4(rc, rs))
+
+
+def test_outputs_of_8_mb_a_row():
+    """More columns than a tile's offsets reach across: every 4096 of them the same weights.
+    One block of k, so the sums are exact in any order."""
+    need_gpu()
+    M, K, N, times = 300, 32, 4096, 1024
+    a, sa, _ = operand(M, K, 1)
+    w, sw, _ = operand(N, K, 2)
+    assert w4.w4a4_gemm_mx4_plan(M, K, N * times) == "skinny" != w4.w4a4_gemm_mx4_plan(M, K, N)
+    out = w4.w4a4_gemm_mx4(a, sa, w.repeat(times, 1), sw.repeat(1, times, 1))
+    assert bool((out.view(M, times, N) == w4.w4a4_gemm_mx4(a, sa, w, sw)[:, None]).all())
