@@ -462,7 +462,7 @@ __device__ __forceinline__ void mx_put_gated(const Mx4GemmArgs& a, v16f (&acc)[M
 // conversion, 8 for its stores.  Tiles of 128 and 64 rows read more LDS per MFMA
 // (a row's step goes at 0.73 and 0.55 of the rate) and are for outputs too few
 // to fill the CUs with larger ones: 16396 rows of 32 experts x 3840 x 2560 127
-// us; 333 x 5376 x 7168 20 us, 126 tiles for 256 CUs.  Gated: 32768 x 3840 x 2560
+// us; 333 x 5376 x 7168 20 us, 168 tiles for 256 CUs.  Gated: 32768 x 3840 x 2560
 // 181 us.
 // Storing a tile's outputs between the next tile's MFMAs, with two sets of
 // accumulators, was slower: the compiler moves them between registers.
