@@ -94,9 +94,13 @@ _SIGNATURES = {
     "w4a4_route_experts": ([_vp, ctypes.c_int, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
                            ctypes.c_int),
     "w4a4_combine_experts": ([_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp], ctypes.c_int),
+    "w4a4_combine_experts_to": ([_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _i64, _i32, _vp, ctypes.c_int, _vp],
+                                ctypes.c_int),
     "w4a4_experts_mx4_workspace_size": ([_i64, _i64, _i64, _i32, _i32, ctypes.c_int], _sz),
     "w4a4_experts_mx4": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_int, _i64, _i32,
                           _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "w4a4_experts_mx4_rows": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_int, _i64, _i32,
+                               _i32, _i32, _vp, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _vp, _sz, _vp], ctypes.c_int),
     "w4a4_linear_noalloc": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i64,
                              _vp, ctypes.c_int, _i32, _vp, _vp, _vp, _i32, _vp, ctypes.c_int, _vp],
                             ctypes.c_int),
@@ -1278,34 +1282,43 @@ def w4a4_route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = Tru
     return weights, experts, rows, pos, offsets
 
 
-def w4a4_combine_experts(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
-    """out[t] = sum_j weights[t, j] * y[pos[t, j]] (pos -1 adds nothing), (T, N) in y's dtype."""
+def w4a4_combine_experts(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
+                         out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[pos[t, j]] (pos -1 adds nothing), (T, N)
+    in y's dtype, or where y is float32 in out_dtype."""
     _need(y, "y", dtypes=_FLOAT)
     _need(pos, "pos", dtypes=(torch.int32,))
     if y.dim() != 2 or pos.dim() != 2 or pos.shape[1] < 1:
         raise ValueError(f"y {tuple(y.shape)} and pos {tuple(pos.shape)} must be (R, N) and (T, k)")
     _need(weights, "weights", tuple(pos.shape), (torch.float32,))
+    out_dtype = out_dtype or y.dtype
+    if out_dtype not in _FLOAT or y.dtype not in (out_dtype, torch.float32):
+        raise ValueError(f"out_dtype {out_dtype} of {y.dtype} rows: their own, or of float32 rows float16/bfloat16")
     _same_device(y, pos=pos, weights=weights)
     R, N = y.shape
     T, k = pos.shape
-    out = torch.empty((T, N), dtype=y.dtype, device=y.device)
-    rc = lib().w4a4_combine_experts(_ptr(y), _DT[y.dtype], R, N, _ptr(pos), _ptr(weights), T, k, _ptr(out),
-                                    _stream(y.device))
+    out = torch.empty((T, N), dtype=out_dtype, device=y.device)
+    rc = lib().w4a4_combine_experts_to(_ptr(y), _DT[y.dtype], R, N, _ptr(pos), _ptr(weights), T, k, _ptr(out),
+                                       _DT[out_dtype], _stream(y.device))
     _check(rc, "w4a4_combine_experts")
     return out
 
 
 def w4a4_experts_mx4_workspace_size(T: int, K: int, F: int, E: int, top_k: int, dtype: torch.dtype) -> int:
+    """Bytes for w4a4_experts_mx4; dtype is that of the experts' rows (rows_dtype, else x's)."""
     return int(lib().w4a4_experts_mx4_workspace_size(T, K, F, E, top_k, _DT[dtype]))
 
 
 def w4a4_experts_mx4(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_codes: torch.Tensor,
                      w13_scales: torch.Tensor, w2_codes: torch.Tensor, w2_scales: torch.Tensor,
                      h: Optional[Hadamard] = None, renormalize: bool = True,
-                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     rows_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """The expert layer on x (..., K) with router logits (T, E): route, quantize
     (rotated by h first if given), gated product with w13 (E, 2 F, K; F gates
-    then F ups), product with w2 (E, K, F), weighted sum per token."""
+    then F ups), product with w2 (E, K, F), weighted sum per token.  The experts'
+    rows wait for the sum in rows_dtype: x's (a 16-bit layer then rounds twice),
+    or float32."""
     lead = _need(x, "x", contiguous=False).shape[:-1]
     x2 = _as_2d(x)
     T, K = x2.shape
@@ -1324,15 +1337,19 @@ def w4a4_experts_mx4(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_code
         raise ValueError(f"top_k={top_k} of {E} experts")
     if out is not None:
         _need(out, "out", (T, K), (x2.dtype,))
+    rows_dtype = rows_dtype or x2.dtype
+    if rows_dtype not in (x2.dtype, torch.float32):
+        raise ValueError(f"rows_dtype {rows_dtype} is not {x2.dtype} or float32")
     _same_device(x2, sign_in=si, sign_out=so, logits=logits, w13_codes=w13_codes, w13_scales=w13_scales,
                  w2_codes=w2_codes, w2_scales=w2_scales, workspace=workspace, out=out)
     dev = x2.device
     if out is None:
         out = torch.empty((T, K), dtype=x2.dtype, device=dev)
-    workspace = _workspace(workspace, int(lib().w4a4_experts_mx4_workspace_size(T, K, F, E, top_k, dt)), dev)
-    rc = lib().w4a4_experts_mx4(
+    workspace = _workspace(workspace, int(lib().w4a4_experts_mx4_workspace_size(T, K, F, E, top_k, _DT[rows_dtype])),
+                           dev)
+    rc = lib().w4a4_experts_mx4_rows(
         _ptr(x2), dt, T, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(logits), _DT[logits.dtype],
         logits.stride(0), E, top_k, int(bool(renormalize)), _ptr(w13_codes), _ptr(w13_scales), F, _ptr(w2_codes),
-        _ptr(w2_scales), _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev))
+        _ptr(w2_scales), _DT[rows_dtype], _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev))
     _check(rc, "w4a4_experts_mx4")
     return out if len(lead) == 1 else out.view(*lead, K)

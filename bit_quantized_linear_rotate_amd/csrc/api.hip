@@ -1145,23 +1145,32 @@ int w4a4_route_experts(const void* logits, int dtype, int64_t T, int64_t stride,
 int w4a4_combine_experts(const void* y, int dtype, int64_t R, int64_t N, const int32_t* pos, const float* weights,
                          int64_t T, int32_t top_k, void* out, void* stream)
 {
+    return w4a4_combine_experts_to(y, dtype, R, N, pos, weights, T, top_k, out, dtype, stream);
+}
+
+int w4a4_combine_experts_to(const void* y, int dtype, int64_t R, int64_t N, const int32_t* pos, const float* weights,
+                            int64_t T, int32_t top_k, void* out, int out_dtype, void* stream)
+{
     if (R < 0 || N < 0 || T < 0) return fail(W4A4_INVALID, "negative size");
-    if (!dtype_ok(dtype)) return fail(W4A4_UNSUPPORTED, "unknown dtype code %d", dtype);
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype))
+        return fail(W4A4_UNSUPPORTED, "unknown dtype code %d, %d", dtype, out_dtype);
+    if (dtype != W4A4_F32 && out_dtype != dtype)
+        return fail(W4A4_UNSUPPORTED, "16-bit rows are combined in their own type");
     if (top_k < 1) return fail(W4A4_INVALID, "top_k=%d", top_k);
     if (R >= (int64_t)1 << 31) return fail(W4A4_UNSUPPORTED, "%lld sorted rows: at most 2^31 - 1", (long long)R);
     if (T == 0 || N == 0) return W4A4_OK;
     if ((R > 0 && !y) || !pos || !weights || !out) return fail(W4A4_INVALID, "a required pointer is NULL");
     const int rc = device_check();
     if (rc) return rc;
-    const CombineArgs a{y, dtype, R, T, N, top_k, pos, weights, out};
+    const CombineArgs a{y, dtype, R, T, N, top_k, pos, weights, out, out_dtype};
     const hipError_t e = launch_combine(a, (hipStream_t)stream);
     return e == hipSuccess ? W4A4_OK : hip_fail(e, "combining launch");
 }
 
-size_t w4a4_experts_mx4_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k, int x_dtype)
+size_t w4a4_experts_mx4_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k, int rows_dtype)
 {
-    if (T <= 0 || K <= 0 || F <= 0 || E <= 0 || top_k <= 0 || !dtype_ok(x_dtype)) return 0;
-    return ExpertsSpace(T, K, F, E, top_k, x_dtype).total;
+    if (T <= 0 || K <= 0 || F <= 0 || E <= 0 || top_k <= 0 || !dtype_ok(rows_dtype)) return 0;
+    return ExpertsSpace(T, K, F, E, top_k, rows_dtype).total;
 }
 
 int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
@@ -1170,14 +1179,28 @@ int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t s
                      const uint8_t* w13_scales, int64_t F, const uint8_t* w2_codes, const uint8_t* w2_scales, void* out,
                      void* workspace, size_t workspace_bytes, void* stream)
 {
+    return w4a4_experts_mx4_rows(x, x_dtype, T, K, stride_m, stride_k, g, sign_in, sign_out, logits, logits_dtype,
+                                 logits_stride, E, top_k, renormalize, w13_codes, w13_scales, F, w2_codes, w2_scales,
+                                 x_dtype, out, workspace, workspace_bytes, stream);
+}
+
+int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                          const int8_t* sign_in, const int8_t* sign_out, const void* logits, int logits_dtype,
+                          int64_t logits_stride, int32_t E, int32_t top_k, int32_t renormalize,
+                          const uint8_t* w13_codes, const uint8_t* w13_scales, int64_t F, const uint8_t* w2_codes,
+                          const uint8_t* w2_scales, int rows_dtype, void* out, void* workspace, size_t workspace_bytes,
+                          void* stream)
+{
     int rc = mx4_quant_validate(x, x_dtype, T, K, stride_m, stride_k, g, sign_in, sign_out);
     if (rc) return rc;
+    if (rows_dtype != x_dtype && rows_dtype != W4A4_F32)
+        return fail(W4A4_UNSUPPORTED, "rows dtype code %d: x's or fp32", rows_dtype);
     if (F < 1 || F % kMxBlock) return fail(W4A4_INVALID, "F=%lld is not a positive multiple of 32", (long long)F);
     if (E < 1 || top_k < 1 || top_k > E) return fail(W4A4_INVALID, "top_k=%d of E=%d experts", top_k, E);
     if (T == 0) return W4A4_OK;
     if (T * top_k >= (int64_t)1 << 28)
         return fail(W4A4_UNSUPPORTED, "T top_k = %lld: at most 2^28 - 1", (long long)(T * top_k));
-    const ExpertsSpace at(T, K, F, E, top_k, x_dtype);
+    const ExpertsSpace at(T, K, F, E, top_k, rows_dtype);
     if (!workspace || workspace_bytes < at.total)
         return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, at.total);
     if ((uintptr_t)workspace % 16) return fail(W4A4_UNSUPPORTED, "the workspace must be 16-byte aligned");
@@ -1200,13 +1223,13 @@ int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t s
     g1.out_scales = ws + at.act_scales;
     rc = mx4_gated_validate(g1);
     if (rc) return rc;
-    Mx4GemmArgs g2{g1.out_codes, g1.out_scales, R, F, K, w2_codes, w2_scales, nullptr, 0, ws + at.y, x_dtype};
+    Mx4GemmArgs g2{g1.out_codes, g1.out_scales, R, F, K, w2_codes, w2_scales, nullptr, 0, ws + at.y, rows_dtype};
     g2.E = E;
     g2.R = R;
     g2.offsets = offsets;
     rc = mx4_grouped_validate(g2);
     if (rc) return rc;
-    const CombineArgs ca{ws + at.y, x_dtype, R, T, K, top_k, pos, weights, out};
+    const CombineArgs ca{ws + at.y, rows_dtype, R, T, K, top_k, pos, weights, out, x_dtype};
     rc = device_check();
     if (rc) return rc;
     hipStream_t st = (hipStream_t)stream;

@@ -85,12 +85,13 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 // out[t] = sum_j weights[t][j] * y[pos[t][j]], fp32, j in order
 struct CombineArgs {
     const void* y;                 // (R, N)
-    int dtype;                     // of y and out
+    int dtype;                     // of y
     int64_t R, T, N;
     int k;
     const int32_t* pos;            // (T, k)
     const float* weights;          // (T, k)
     void* out;                     // (T, N)
+    int out_dtype;                 // dtype, or any where that is fp32
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
 

@@ -259,14 +259,15 @@ template <int DT> hipError_t route_dt(const RouteArgs& a, hipStream_t st)
 // once.  8 (fp32: 4) columns per thread, one token per workgroup row.  Bound by
 // memory, y being read once: 8192 tokens of 4 rows of 3840 bf16 (315 MB) 58.6
 // us = 5.4 TB/s, a copy's rate.
-// (In the expert layer y is in the layer's 16-bit type, a second rounding next
-// to the output's: 2^-9 of a value, where its four-bit operands are 2^-4 off;
-// in fp32 the layer's largest array would be twice as large: 504 MB more to move,
-// 100 us on 430, at 8192 tokens.)
-template <int DT, bool VEC> __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a)
+// (In the expert layer y is in the layer's 16-bit type unless the caller asks
+// for fp32: a second rounding next to the output's, 2^-9 of a value, where its
+// four-bit operands are 2^-4 off.  In fp32 the layer's largest array is twice as
+// large: 504 MB more to move at 8192 tokens.)
+template <int DT, int ODT, bool VEC> __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a)
 {
     constexpr int V = VEC ? (DT == F32 ? 4 : 8) : 1;
     typedef unsigned v4u __attribute__((ext_vector_type(4)));
+    typedef unsigned v2u __attribute__((ext_vector_type(2)));
     const int64_t pieces = (a.N + V - 1) / V;
     const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (n >= pieces) return;
@@ -292,29 +293,32 @@ template <int DT, bool VEC> __global__ __launch_bounds__(256) void combine_kerne
             }
         }
         if constexpr (!VEC) {
-            store_any(DT, a.out, t * a.N + n, acc[0]);
-        } else if constexpr (DT == F32) {
+            store_any(ODT, a.out, t * a.N + n, acc[0]);
+        } else if constexpr (ODT == F32) {
             ((v4u*)a.out)[t * pieces + n] = (v4u){__float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]),
                                                   __float_as_uint(acc[3])};
+        } else if constexpr (DT == F32) {
+            ((v2u*)a.out)[t * pieces + n] = (v2u){f32_to_h<ODT>(acc[0]) | ((uint32_t)f32_to_h<ODT>(acc[1]) << 16),
+                                                  f32_to_h<ODT>(acc[2]) | ((uint32_t)f32_to_h<ODT>(acc[3]) << 16)};
         } else {
             v4u o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = f32_to_h<DT>(acc[2 * i]) | ((uint32_t)f32_to_h<DT>(acc[2 * i + 1]) << 16);
+            for (int i = 0; i < 4; ++i) o[i] = f32_to_h<ODT>(acc[2 * i]) | ((uint32_t)f32_to_h<ODT>(acc[2 * i + 1]) << 16);
             ((v4u*)a.out)[t * pieces + n] = o;
         }
     }
 }
 
-template <int DT> hipError_t combine_dt(const CombineArgs& a, hipStream_t st)
+template <int DT, int ODT> hipError_t combine_dt(const CombineArgs& a, hipStream_t st)
 {
     const int v = DT == F32 ? 4 : 8;
     const bool vec = a.N % v == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.out % 16 == 0;
     const int64_t pieces = vec ? a.N / v : a.N;
     const dim3 grid((unsigned)((pieces + 255) / 256), (unsigned)(a.T < 65535 ? a.T : 65535));
     if (vec)
-        hipLaunchKernelGGL((combine_kernel<DT, true>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((combine_kernel<DT, ODT, true>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((combine_kernel<DT, false>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((combine_kernel<DT, ODT, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -340,10 +344,17 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st)
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st)
 {
-    switch (a.dtype) {
-    case F32: return combine_dt<F32>(a, st);
-    case F16: return combine_dt<F16>(a, st);
-    case BF16: return combine_dt<BF16>(a, st);
+    if (a.dtype == F32) {
+        switch (a.out_dtype) {
+        case F32: return combine_dt<F32, F32>(a, st);
+        case F16: return combine_dt<F32, F16>(a, st);
+        case BF16: return combine_dt<F32, BF16>(a, st);
+        }
+    } else if (a.dtype == a.out_dtype) {
+        switch (a.dtype) {
+        case F16: return combine_dt<F16, F16>(a, st);
+        case BF16: return combine_dt<BF16, BF16>(a, st);
+        }
     }
     return hipErrorNotSupported;
 }

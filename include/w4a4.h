@@ -376,10 +376,14 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
  *   w4a4_route_experts_workspace_size(T, E) bytes (0 for few tokens).
  * w4a4_combine_experts: out[t] = sum_j weights[t][j] * y[pos[t][j]] in fp32, j
  *   in order (pos -1 adds nothing), y (R, N) and out (T, N) in one dtype.
+ * w4a4_combine_experts_to: the same with y in fp32 and out in any dtype.
  * w4a4_experts_mx4: route, quantise, gated product (w13: (E, 2 F, K), gates
  *   first), product (w2: (E, K, F)), combine; the experts' rows are kept in
- *   x_dtype between the last two.  Workspace of
- *   w4a4_experts_mx4_workspace_size bytes, 16-byte aligned.
+ *   x_dtype between the last two, so a 16-bit layer rounds twice.  Workspace of
+ *   w4a4_experts_mx4_workspace_size(.., x_dtype) bytes, 16-byte aligned.
+ * w4a4_experts_mx4_rows: the same with the experts' rows kept in rows_dtype,
+ *   x_dtype or W4A4_F32 (one rounding, to out); rows_dtype also in the
+ *   workspace's size.
  */
 size_t w4a4_mx4_scales_size(int64_t rows, int64_t K);
 int w4a4_quantize_mx4(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,
@@ -411,8 +415,11 @@ int w4a4_route_experts(const void* logits, int dtype, int64_t T, int64_t stride,
                        size_t workspace_bytes, void* stream);
 int w4a4_combine_experts(const void* y, int dtype, int64_t R, int64_t N, const int32_t* pos,
                          const float* weights, int64_t T, int32_t top_k, void* out, void* stream);
+int w4a4_combine_experts_to(const void* y, int dtype, int64_t R, int64_t N, const int32_t* pos,
+                            const float* weights, int64_t T, int32_t top_k, void* out, int out_dtype,
+                            void* stream);
 size_t w4a4_experts_mx4_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k,
-                                       int x_dtype);
+                                       int rows_dtype);
 int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m,
                      int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
                      const void* logits, int logits_dtype, int64_t logits_stride, int32_t E,
@@ -420,6 +427,13 @@ int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t s
                      const uint8_t* w13_scales, int64_t F, const uint8_t* w2_codes,
                      const uint8_t* w2_scales, void* out, void* workspace, size_t workspace_bytes,
                      void* stream);
+int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m,
+                          int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                          const void* logits, int logits_dtype, int64_t logits_stride, int32_t E,
+                          int32_t top_k, int32_t renormalize, const uint8_t* w13_codes,
+                          const uint8_t* w13_scales, int64_t F, const uint8_t* w2_codes,
+                          const uint8_t* w2_scales, int rows_dtype, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /*
  * w4a4_linear for callers that cannot allocate device memory (code under
