@@ -80,23 +80,17 @@ template <int G> constexpr float inv_sqrt()
 // g = 16, 64, 256: 1 / sqrt(g) = 2^-k, an exponent's worth; else 0
 template <int G> constexpr int inv_sqrt_exp() { return G == 16 ? 2 : G == 64 ? 3 : G == 256 ? 4 : 0; }
 
-// the fp32 bits of the largest magnitude of sixteen values, NaN and infinity
-// on top
-template <int G> __device__ __forceinline__ uint32_t amax_bits(const float (&v)[16])
+// The fp32 bits of the largest magnitude of sixteen values, infinity and NaN on
+// top.  The maximum keeps a NaN wherever it stands (fmaxf would drop it beside a
+// number): butterflies of finite values can overflow to infinities and then
+// cancel to a NaN in a block that is otherwise finite.
+__device__ __forceinline__ uint32_t amax_bits(const float (&v)[16])
 {
-    if constexpr (G >= 32) {
-        // A NaN or an infinity leaves nothing finite in its rotation group, so
-        // not in the block either: the float maximum, which passes over NaN
-        // beside numbers, sees it.
-        float m = 0.0f;
+    float m = __builtin_elementwise_maximum(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) m = e ? fmaxf(fmaxf(m, fabsf(v[e])), fabsf(v[e + 1])) : fmaxf(fabsf(v[0]), fabsf(v[1]));
-        return __float_as_uint(m);
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
-    return m;
+    for (int e = 2; e < 16; e += 2)
+        m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(v[e])), fabsf(v[e + 1]));
+    return __float_as_uint(m) & 0x7fffffffu;
 }
 
 // Sixteen lanes hold 256 consecutive k of a row, sixteen per lane (the more a
@@ -176,7 +170,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4QuantArgs a)
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = mul_rn(v[e], inv_sqrt<G>());
         }
-        uint32_t m = amax_bits<G>(v);
+        uint32_t m = amax_bits(v);
         m = max(m, mq_xor<1>(m));
         int k = KEXP;   // y = v * 2^-k
         if constexpr (KEXP > 0) {
@@ -184,7 +178,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4QuantArgs a)
             if (__any(m && m < (40u << 23))) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = mul_rn(v[e], inv_sqrt<G>());
-                m = amax_bits<G>(v);
+                m = amax_bits(v);
                 m = max(m, mq_xor<1>(m));
                 k = 0;
             }
