@@ -1224,7 +1224,7 @@ def w4a4_grouped_gemm_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: to
     """MX4 products grouped by expert: sorted row i (of expert e's
     offsets[e] .. offsets[e + 1] - 1; int32 (E + 1,) on the device) is row
     rows[i] of codes (rows None: row i) and meets expert e's weights (E, N, K).
-    Returns (R, N); rows from offsets[E] on are zeros."""
+    Returns (R, N); rows before offsets[0] and from offsets[E] on are zeros."""
     M, K, E, N, R = _grouped_checks(codes, scales, w_codes, w_scales, offsets, rows, bias)
     if out_dtype not in _FLOAT:
         raise ValueError(f"out_dtype {out_dtype} is not float32/float16/bfloat16")

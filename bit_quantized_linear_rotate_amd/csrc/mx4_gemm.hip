@@ -202,24 +202,23 @@ __device__ __forceinline__ void mx_rows_of(const Mx4GemmArgs& a, int tile, int t
     }
 }
 
-// Zeros for the sorted rows that no expert owns (from offsets[E] on), spread
-// over the workgroups that have no tile.
+// Zeros for the sorted rows that no expert owns (before offsets[0] and from
+// offsets[E] on), spread over the workgroups that have no tile.
 __device__ __forceinline__ void mx_zero_rows(const Mx4GemmArgs& a, int64_t part, int64_t parts)
 {
-    const int64_t from = mx_offset(a, a.E);
+    // number i of these rows' elements, n to a row: one of a row before the
+    // first expert's, or one past the last's
+    const int64_t first = mx_offset(a, 0), from = max(mx_offset(a, a.E), first), rows = first + a.R - from;
+    const int64_t start = part * blockDim.x + threadIdx.x, step = parts * blockDim.x;
+    auto at = [&](int64_t i, int64_t n) { return i < first * n ? i : i + (from - first) * n; };
     if (a.out_codes) {
-        const int64_t F = a.N / 2, wide = F / 2;
-        for (int64_t i = from * wide + part * blockDim.x + threadIdx.x; i < a.R * wide; i += parts * blockDim.x)
-            a.out_codes[i] = 0;
-        const int64_t slabs = (F + 255) / 256, n = (a.R - from) * 8;
-        for (int64_t i = part * blockDim.x + threadIdx.x; i < n * slabs; i += parts * blockDim.x)
-            a.out_scales[(i / n * a.R + from) * 8 + i % n] = 0;
+        const int64_t F = a.N / 2, wide = F / 2, slabs = (F + 255) / 256, n = rows * 8;
+        for (int64_t i = start; i < rows * wide; i += step) a.out_codes[at(i, wide)] = 0;
+        for (int64_t i = start; i < n * slabs; i += step) a.out_scales[i / n * a.R * 8 + at(i % n, 8)] = 0;
     } else {
-        const int esz = a.out_dtype == F32 ? 4 : 2;
+        const int64_t wide = a.N * (a.out_dtype == F32 ? 2 : 1);
         uint16_t* o = (uint16_t*)a.out;
-        const int64_t end = a.R * a.N * (esz / 2);
-        for (int64_t i = from * a.N * (esz / 2) + part * blockDim.x + threadIdx.x; i < end; i += parts * blockDim.x)
-            o[i] = 0;
+        for (int64_t i = start; i < rows * wide; i += step) o[at(i, wide)] = 0;
     }
 }
 

@@ -357,8 +357,8 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
  *   offsets[e + 1] - 1 (device array of E + 1, not decreasing); sorted row i
  *   is row rows[i] of the (M, K) codes (rows NULL: row i, and M = R) and meets
  *   expert e's weights (E, N, K/2), scales (E, slabs, N, 8), bias (E, N).  An
- *   index outside [0, M) counts as a zero row.  Rows from offsets[E] on are
- *   written as zeros.
+ *   index outside [0, M) counts as a zero row.  Rows before offsets[0] and from
+ *   offsets[E] on are written as zeros.
  * w4a4_grouped_gated_mx4: the same product with N/2 gates followed by N/2 ups
  *   (N % 64 == 0); the result is the MX4 form of silu(gate) * up, taken from
  *   the fp32 sums: out_codes (R, N/4), out_scales (slabs of N/2, R, 8).
