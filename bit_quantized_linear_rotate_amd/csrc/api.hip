@@ -231,7 +231,9 @@ int route_validate(const RouteArgs& a)
     if (a.E > kRouteMaxExperts || a.k > kRouteMaxTopK)
         return fail(W4A4_UNSUPPORTED, "E=%d, top_k=%d: at most %d and %d", a.E, a.k, kRouteMaxExperts, kRouteMaxTopK);
     if (a.stride < a.E && a.T > 1) return fail(W4A4_INVALID, "logits rows overlap (stride %lld)", (long long)a.stride);
-    if (a.T * a.k >= (int64_t)1 << 31) return fail(W4A4_UNSUPPORTED, "T top_k = %lld: at most 2^31 - 1", (long long)(a.T * a.k));
+    // (T by itself first: its product with top_k could pass 64 bits)
+    if (a.T >= (int64_t)1 << 31 || a.T * a.k >= (int64_t)1 << 31)
+        return fail(W4A4_UNSUPPORTED, "T=%lld, top_k=%d: T top_k at most 2^31 - 1", (long long)a.T, a.k);
     if (!a.offsets) return fail(W4A4_INVALID, "offsets is NULL");
     if (a.T > 0 && (!a.logits || !a.weights || !a.experts || !a.rows || !a.pos))
         return fail(W4A4_INVALID, "a required pointer is NULL");

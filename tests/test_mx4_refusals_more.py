@@ -1,5 +1,5 @@
-"""CPU tests of refusals of the expert layer's row type: by the binding (ValueError) and
-by the C ABI (status codes), before any device access."""
+"""CPU tests of further refusals of the MX4 entry points, by the binding (ValueError) and
+by the C ABI (status codes), before any device access; and of host-only choices."""
 import os
 
 import pytest
@@ -28,3 +28,10 @@ def test_row_types_are_refused():
     small = b.w4a4_experts_mx4_workspace_size(M, K, 64, E, 2, BF)
     need = b.w4a4_experts_mx4_workspace_size(M, K, 64, E, 2, torch.float32)
     assert need > small and rows(0, need - 1) == b.INVALID and b"workspace" in L.w4a4_last_error()
+
+
+def test_token_counts_past_any_memory_are_refused():
+    L = b.lib()
+    for T, k in ((1 << 62, 4), (1 << 61, 8), (1 << 31, 1), (1 << 30, 2)):
+        rc = L.w4a4_route_experts(FAKE, 0, T, 8, 8, k, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, None)
+        assert rc == b.UNSUPPORTED and b"top_k" in L.w4a4_last_error()
