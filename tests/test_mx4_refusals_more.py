@@ -35,3 +35,12 @@ def test_token_counts_past_any_memory_are_refused():
     for T, k in ((1 << 62, 4), (1 << 61, 8), (1 << 31, 1), (1 << 30, 2)):
         rc = L.w4a4_route_experts(FAKE, 0, T, 8, 8, k, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, None)
         assert rc == b.UNSUPPORTED and b"top_k" in L.w4a4_last_error()
+
+
+def test_one_row_of_one_expert_is_the_skinny_kernels():
+    """However narrow the output: a tile of 64 x 256 is never cheaper than 16 columns a wave."""
+    for K in (512, 1824, 3840):
+        for n in (64, 96, 256):
+            for experts in (0, 1, 2):
+                assert b.w4a4_gemm_mx4_plan(1, K, n, experts) == "skinny", (K, n, experts)
+            assert b.w4a4_gemm_mx4_plan(1, K, n, 1, True) == "skinny", (K, n)
