@@ -102,10 +102,9 @@ __device__ __forceinline__ void mx_here(v16f& c) { asm volatile("" : "+a"(c)); }
 
 // ---- which rows a workgroup takes --------------------------------------------
 struct MxRows {
-    int64_t m0;   // first (sorted) row
-    int rows;     // rows of the tile, 0: none
-    int e;        // expert
-    int m, cm;    // tile of the expert, and how many it has
+    int64_t m0;   // the expert's first (sorted) row
+    int rows;     // rows of the expert
+    int e;        // expert, -1: none
     int64_t before;   // tiles of the experts before it
 };
 
@@ -128,11 +127,10 @@ __device__ __forceinline__ int mx_scan(int v)
     return v;
 }
 
-// The row tile `idx` of the list of all experts' tiles of BM rows (idx < 0:
-// only count).  Every wave scans the offsets, 64 experts at a time.  Returns
-// the number of tiles.
-template <int BM, bool BY_TILE> __device__ __forceinline__ int64_t mx_find(const Mx4GemmArgs& a, int64_t idx, int64_t per,
-                                                                         MxRows& r)
+// The expert that has row tile `idx` of the list of all experts' tiles of BM
+// rows (BY_TILE; else only count).  Every wave scans the offsets, 64 experts at
+// a time.  Returns the number of tiles (of those looked at).
+template <int BM, bool BY_TILE> __device__ __forceinline__ int64_t mx_find(const Mx4GemmArgs& a, int64_t idx, MxRows& r)
 {
     const int lane = threadIdx.x & 63;
     int64_t base = 0;
@@ -149,14 +147,13 @@ template <int BM, bool BY_TILE> __device__ __forceinline__ int64_t mx_find(const
         const int cm = (cnt + BM - 1) / BM;
         const int inc = mx_scan(cm);
         const int sum = __builtin_amdgcn_readlane(inc, 63);
-        if (BY_TILE && r.e < 0 && idx >= base * per && idx < (base + sum) * per) {
-            const unsigned long long hit = __ballot((base + inc) * per > idx);
+        if (BY_TILE && r.e < 0 && idx >= base && idx < base + sum) {
+            const unsigned long long hit = __ballot(base + inc > idx);
             const int w = __builtin_ctzll(hit);
             r.e = e0 + w;
-            r.cm = __builtin_amdgcn_readlane(cm, w);
-            r.before = base + __builtin_amdgcn_readlane(inc, w) - r.cm;
+            r.before = base + __builtin_amdgcn_readlane(inc, w) - __builtin_amdgcn_readlane(cm, w);
             r.m0 = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)lo, w);
-            r.rows = __builtin_amdgcn_readlane(cnt, w);   // of the expert; the caller picks the tile
+            r.rows = __builtin_amdgcn_readlane(cnt, w);
             return base + sum;
         }
         base += sum;
@@ -376,7 +373,7 @@ template <int MT, bool BIAS>
 __device__ __forceinline__ void mx_put_gated(const Mx4GemmArgs& a, v16f (&acc)[MT][4], int64_t m0, int row0, int rows, int tn,
                                              bool last, int wn, int h, int e)
 {
-    const int64_t F = a.N >> 1, R = a.E ? a.R : a.M;
+    const int64_t F = a.N >> 1, R = a.R;
     const int pitch = (int)(F >> 1);
     const __amdgpu_buffer_rsrc_t rc = mx_rsrc(mx_uniform(a.out_codes + m0 * pitch), (int64_t)rows * pitch);
     const __amdgpu_buffer_rsrc_t rs = mx_rsrc(mx_uniform(a.out_scales + ((int64_t)(tn >> 1) * R + m0) * 8), rows * 8);
@@ -496,7 +493,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
     int ntiles;
     if constexpr (GROUPED) {
         MxRows r;
-        ntiles = (int)mx_find<BM, false>(a, 0, 1, r) * tiles_n;
+        ntiles = (int)mx_find<BM, false>(a, 0, r) * tiles_n;
         mx_zero_rows(a, blockIdx.x, gridDim.x);
     } else {
         ntiles = tiles_m * tiles_n;
@@ -811,7 +808,7 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
     int rows, e = 0;
     if constexpr (GROUPED) {
         MxRows r;
-        const int64_t total = mx_find<16 * MT, true>(a, blockIdx.y, 1, r);
+        const int64_t total = mx_find<16 * MT, true>(a, blockIdx.y, r);
         if (r.e < 0) {
             mx_zero_rows(a, (int64_t)(blockIdx.y - total) * gridDim.x + blockIdx.x, (int64_t)(gridDim.y - total) * gridDim.x);
             return;
@@ -902,7 +899,7 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
     if constexpr (GATED) {
         // a half wave takes the 32 results of one row of one group
         const int c = tid & 31;
-        const int64_t R = GROUPED ? a.R : a.M;
+        const int64_t R = a.R;
         for (int i = tid >> 5; i < 16 * MT * CG; i += 16) {
             const int row = i % (16 * MT), g_ = i / (16 * MT), mt = row >> 4;
             const int64_t f = ((int64_t)blockIdx.x * CG + g_) * 32 + c;
@@ -1010,7 +1007,6 @@ template <int MT> hipError_t launch_skinny(const Mx4GemmArgs& a, hipStream_t st)
 
 namespace {
 
-// Rows of a skinny pass, and 16-column tiles per wave
 // Estimated microseconds of each kernel.  Tiles: the 256 workgroups take them
 // in rounds; a step (256 k) of a 64, 128, 256 row tile measured 0.66, 1.0,
 // 1.46 us with all CUs busy, and a tile's beginning and end 3.7, 4.2, 9.4 us

@@ -29,12 +29,6 @@ namespace {
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mq_rsrc(const void* base, uint64_t bytes)
-{
-    const uint32_t n = bytes > 0xffffffffull ? 0xffffffffu : (uint32_t)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)n, 0x00020000);
-}
-
 // the value of the lane whose index differs in bit D (D = 1, 2, 4, 8)
 template <int D> __device__ __forceinline__ uint32_t mq_xor(uint32_t v)
 {
