@@ -188,6 +188,26 @@ def test_strided_activations_through_the_layers():
         assert torch.equal(w4.w4a4_experts_mx4(v, many[:, 1:E + 1], 2, w13, s13, w2, s2, h=h), ref[1])
 
 
+@pytest.mark.parametrize("E,k", [(8, 2), (300, 20)])
+def test_route_infinite_logits(E, k):
+    """An infinite logit is taken first, and leaves no weights; the lowest finite value is a
+    logit like others, and a row of them an even one."""
+    need_gpu()
+    l = logits_of(40, E, "f32", 1)
+    l[7, 3] = l[9, 2] = l[9, 5] = float("inf")
+    l[11], l[12] = torch.finfo(torch.float32).min, float("-inf")
+    l[12, 4] = torch.finfo(torch.float32).min
+    for renorm in (True, False):
+        w, e, rows, pos, off = (t.cpu() for t in w4.w4a4_route_experts(l, k, renormalize=renorm))
+        assert e[7, 0] == 3 and e[9, :2].tolist() == [2, 5] and w[7].isnan().all() and w[9].isnan().all()
+        assert e[11].tolist() == list(range(k)) and torch.equal(w[11], torch.full((k,), 1 / (k if renorm else E)))
+        assert e[12].tolist() == [4] + [-1] * (k - 1) and w[12].tolist() == [1.0] + [0.0] * (k - 1)
+        others = [t for t in range(40) if t not in (7, 9)]
+        ref = mx4.route(as64(l[others]), k, renorm)
+        assert np.array_equal(e[others].numpy(), ref[1])
+        assert (np.abs(w[others].double().numpy() - ref[0]) <= (E + 64) * 2.0 ** -24 * ref[0]).all()
+
+
 @pytest.mark.parametrize("T", [16, 300])
 def test_routing_and_layer_replay_in_a_graph(T):
     """T = 300: routing in several chunks, two launches."""
