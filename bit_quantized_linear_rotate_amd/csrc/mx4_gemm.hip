@@ -96,8 +96,11 @@ __device__ __forceinline__ void mx_settle(v16f (&c)[4])
     asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
 }
 
-// An accumulator leaves its accumulation registers no earlier than here (the
-// compiler would copy all of them out ahead of the epilogue's branches).
+// An accumulator leaves the accumulation registers no earlier than here (the
+// compiler would copy all of them out ahead of the epilogue's branches).  It
+// still moves them among each other: 240 moves before most of the epilogues of
+// 256-row tiles, which are branches of one kernel, and in the grouped one 16
+// registers out to scratch and back, once a tile.
 __device__ __forceinline__ void mx_here(v16f& c) { asm volatile("" : "+a"(c)); }
 
 // ---- which rows a workgroup takes --------------------------------------------
@@ -219,10 +222,12 @@ __device__ __forceinline__ void mx_zero_rows(const Mx4GemmArgs& a, int64_t part,
     }
 }
 
-// silu(g) * u in fp32: g (1 / (1 + exp(-g))) u.  The reciprocal is the
-// hardware's (1 ulp; the result is rounded to four bits next): a rounded
-// division is ten instructions a value, 2 us a tile of 256 x 128 results.  Where
-// it falls below 2^-126 (g < -87) it is zero.
+// silu(g) * u in fp32: g (1 / (1 + exp(-g))) u, rounded to four bits next.  exp is
+// 2^(-g log2(e)), whose argument is rounded twice, so off by up to |g| 2^-23 of
+// itself; the power and the reciprocal are the hardware's (1 ulp; a rounded
+// division is ten instructions a value, 2 us a tile of 256 x 128 results).  In all
+// (|g| + 4) 2^-23 of the value.  Where the reciprocal falls below 2^-126 (g < -87)
+// it is zero.
 __device__ __forceinline__ float mx_gated(float g, float u)
 {
     return mul_rn(mul_rn(g, __builtin_amdgcn_rcpf(add_rn(1.0f, __expf(-g)))), u);
@@ -458,8 +463,8 @@ __device__ __forceinline__ void mx_put_gated(const Mx4GemmArgs& a, v16f (&acc)[M
 // conversion, 8 for its stores.  Tiles of 128 and 64 rows read more LDS per MFMA
 // (a row's step goes at 0.73 and 0.55 of the rate) and are for outputs too few
 // to fill the CUs with larger ones: 16396 rows of 32 experts x 3840 x 2560 127
-// us; 333 x 5376 x 7168 20 us, 168 tiles for 256 CUs.  Gated: 32768 x 3840 x 2560
-// 181 us.
+// us; 333 x 5376 x 7168 in fp32 24 us, 168 tiles for 256 CUs.  Gated: 32768 x 3840
+// x 2560 183 us.
 // Storing a tile's outputs between the next tile's MFMAs, with two sets of
 // accumulators, was slower: the compiler moves them between registers.
 template <int BM, bool GROUPED, bool GATED>
@@ -787,8 +792,8 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4GemmArgs a, int til
 // ups, one block of results); 8 / KW groups lie side by side.  The waves'
 // partial sums meet in LDS and are added in wave order.
 // Bound by the weights' bytes and, up to a few megabytes of them, by latency:
-// 3840 x 3840 weights (7.8 MB) with one row 4.1 us, 10240 x 10240 (56 MB) 14.9
-// us = 3.7 TB/s; 64 rows 27.4 us, each column group reading the rows again.
+// 3840 x 3840 weights (7.8 MB) with one row 4.2 us, 10240 x 10240 (56 MB) 14.9 to
+// 15.6 us = 3.7 TB/s; 64 rows 27.4 to 28.4 us, each column group reading the rows again.
 constexpr int kSkinnyWaves = 8;
 template <int MT, int NT, int KW, bool GROUPED, bool GATED>
 __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4GemmArgs a)
@@ -1011,10 +1016,12 @@ namespace {
 // in rounds; a step (256 k) of a 64, 128, 256 row tile measured 0.66, 1.0,
 // 1.46 us with all CUs busy, and a tile's beginning and end 3.7, 4.2, 9.4 us
 // (16384 x 2560 outputs at K = 3840 and 7680: 136 and 235, 96 and 171, 95 and
-// 161 us).  Skinny: 2.5 us, then weights at 5 TB/s and, for each column group,
+// 161 us; at other shapes the choice can be wrong: 768 rows of each of 8 experts
+// of 3840 x 2560 take tiles of 64 rows, 54 us where 128 and 256 take 42 and 40).
+// Skinny: 2.5 us, then weights at 5 TB/s and, for each column group,
 // the rows again at 6 TB/s (10240 x 10240 weights with 1, 16, 32, 64 rows:
-// 14.9, 18.3, 19.9, 27.4 us).  Groups of unknown size are taken to fill half
-// of their last tile.
+// 14.9, 18.3, 19.9, 27.4 us).  The groups' sizes are on the device: all are
+// taken to have the mean, and to fill half of their last tile.
 double tile_us(const Mx4GemmArgs& a, int bm, double step, double ends)
 {
     const double tn = a.out_codes ? (double)((a.N / 2 + 127) / 128) : (double)((a.N + 255) / 256);
@@ -1050,8 +1057,12 @@ int mx4_gemm_path(const Mx4GemmArgs& a)
     const double t[4] = {skinny_us(a), tile_us(a, 64, 0.66, 3.7), tile_us(a, 128, 1.0, 4.2), tile_us(a, 256, 1.46, 9.4)};
     const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
     // Tiles of 256 rows are two steps ahead in their weights, the others three:
-    // not enough where a group's weights serve a few tiles only (32 experts of
-    // 3840 x 2560: 8192 rows 96 us against 73 with 128, 32768 rows 203 : 212).
+    // not enough where a group's weights serve a few tiles only.  Ragged groups
+    // of 32 experts of 3840 x 2560 with a mean of 384, 512, 768, 1024, 1536 rows:
+    // 94, 116, 169, 220, 325 us with 128 rows a tile, 97, 134, 178, 222, 313 with
+    // 256; of 16 of 7680 x 2560 93, 101, 164, 201, 285 and 101, 111, 171, 182,
+    // 261.  (Gated with 768 rows 156 : 144, and equal groups can go the other way:
+    // 768 rows 167 : 152, 512 104 : 111.)
     const int last = a.E && rows < 1024 ? kMx4Tile128 : kMx4Tile256;
     int best = kMx4Tile64;
     for (int i = kMx4Tile128; i <= last; ++i)

@@ -341,6 +341,10 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
  *   at (s * rows + r) * 8 + b, scales k = 256 s + 32 b .. + 31; bytes past
  *   K/32 are zero; 4-byte aligned.  w4a4_mx4_scales_size(rows, K) bytes.
  *   K is a multiple of 32, at most 2^24; at most 2^28 rows.
+ *   The products refuse (W4A4_UNSUPPORTED) operands of more than 2^31 bytes of
+ *   scales (an expert's, for weights), codes of more than 2^31 bytes behind a
+ *   row index (so the expert layer's x), and outputs of R x N (M x N) with
+ *   (R / 64 + E + 1) (N / 128 + 1) >= 2^23.
  *
  * w4a4_quantize_mx4: rows of x (any strides; 16-byte aligned contiguous rows
  *   take wide loads) to MX4.  g > 0 first rotates groups of g (a power of two
@@ -372,14 +376,16 @@ int w4a4_linear_bf6(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
  *   (renormalize != 0) or over all E.  The (token, choice) slots sorted by
  *   expert, in slot order within one: offsets (E + 1), rows (T * top_k) the
  *   token of each sorted row (-1 past the last), pos (T, top_k) the sorted row
- *   of each slot.  E <= 1024, top_k <= 32.  A workspace of
+ *   of each slot.  E <= 1024, top_k <= 32, T * top_k < 2^31.  A logit of +inf
+ *   makes its token's weights NaN.  A workspace of
  *   w4a4_route_experts_workspace_size(T, E) bytes (0 for few tokens).
  * w4a4_combine_experts: out[t] = sum_j weights[t][j] * y[pos[t][j]] in fp32, j
  *   in order (pos -1 adds nothing), y (R, N) and out (T, N) in one dtype.
  * w4a4_combine_experts_to: the same with y in fp32 and out in any dtype.
  * w4a4_experts_mx4: route, quantise, gated product (w13: (E, 2 F, K), gates
  *   first), product (w2: (E, K, F)), combine; the experts' rows are kept in
- *   x_dtype between the last two, so a 16-bit layer rounds twice.  Workspace of
+ *   x_dtype between the last two, so a 16-bit layer rounds twice.  No biases
+ *   (the parts take them); T * top_k < 2^28.  Workspace of
  *   w4a4_experts_mx4_workspace_size(.., x_dtype) bytes, 16-byte aligned.
  * w4a4_experts_mx4_rows: the same with the experts' rows kept in rows_dtype,
  *   x_dtype or W4A4_F32 (one rounding, to out); rows_dtype also in the
