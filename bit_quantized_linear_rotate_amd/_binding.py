@@ -101,6 +101,26 @@ _SIGNATURES = {
                           _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "w4a4_experts_mx4_rows": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_int, _i64, _i32,
                                _i32, _i32, _vp, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "w8a8_quantize_fp8": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "w8a8_quantize_weights_fp8": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp,
+                                   _vp], ctypes.c_int),
+    "w8a8_dequantize_fp8": ([_vp, _vp, _i64, _i64, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "w8a8_dequantize_weights_fp8": ([_vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "w8a8_gemm_fp8": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "w8a8_gemm_fp8_plan": ([_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
+    "w8a8_linear_fp8_workspace_size": ([_i64, _i64], _sz),
+    "w8a8_linear_fp8": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
+                         ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "w8a8_grouped_gemm_fp8": ([_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp,
+                               ctypes.c_int, _vp], ctypes.c_int),
+    "w8a8_grouped_gated_fp8": ([_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp,
+                                _vp, _vp], ctypes.c_int),
+    "w4a4_route_experts_scored": ([_vp, ctypes.c_int, _i64, _i64, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32,
+                                   ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "w8a8_experts_fp8_workspace_size": ([_i64, _i64, _i64, _i32, _i32, ctypes.c_int], _sz),
+    "w8a8_experts_fp8": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, ctypes.c_int, _i64, _i32,
+                          _i32, _i32, _vp, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _i64, _vp, _vp,
+                          ctypes.c_int, _vp, _vp, _sz, _vp], ctypes.c_int),
     "w4a4_linear_noalloc": ([_vp, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i64,
                              _vp, ctypes.c_int, _i32, _vp, _vp, _vp, _i32, _vp, ctypes.c_int, _vp],
                             ctypes.c_int),
@@ -1352,4 +1372,346 @@ def w4a4_experts_mx4(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_code
         logits.stride(0), E, top_k, int(bool(renormalize)), _ptr(w13_codes), _ptr(w13_scales), F, _ptr(w2_codes),
         _ptr(w2_scales), _DT[rows_dtype], _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev))
     _check(rc, "w4a4_experts_mx4")
+    return out if len(lead) == 1 else out.view(*lead, K)
+
+
+# ---- block-scaled 8-bit floating point (fp8) --------------------------------------
+
+FP8_KERNELS = {0: "skinny", 1: "tile64", 2: "tile128", 3: "tile256"}
+_E4M3 = torch.float8_e4m3fn
+
+
+def _call(name: str, dev, *args):
+    """One library call on `dev`'s current stream, with `dev` the current device."""
+    if dev.index == torch.cuda.current_device():
+        rc = getattr(lib(), name)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(*args, _stream(dev))
+    _check(rc, name)
+
+
+def _fp8_blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _fp8_rows(codes, scales):
+    """Layout check of quantized rows: codes (M, K), scales (ceil(K/128), M); returns (M, K)."""
+    _need(codes, "codes", dtypes=(_E4M3,))
+    if codes.dim() != 2:
+        raise ValueError(f"codes has shape {tuple(codes.shape)}, expected (M, K)")
+    M, K = codes.shape
+    _fp8_width(K)
+    _need(scales, "scales", (_fp8_blocks(K), M), (torch.float32,))
+    return M, K
+
+
+def _fp8_weights(codes, scales, codes_name: str, scales_name: str, lead: int = 0):
+    """Layout check of quantized weights: codes (.., N, K), scales (.., ceil(N/128),
+    ceil(K/128)), `lead` leading dimensions; returns (N, K)."""
+    _need(codes, codes_name, dtypes=(_E4M3,))
+    if codes.dim() != 2 + lead:
+        raise ValueError(f"{codes_name} has shape {tuple(codes.shape)}, expected {2 + lead} dimensions")
+    N, K = codes.shape[-2:]
+    _fp8_width(K)
+    _need(scales, scales_name, (*codes.shape[:lead], _fp8_blocks(N), _fp8_blocks(K)), (torch.float32,))
+    return N, K
+
+
+def _fp8_width(K: int):
+    if K % 16:
+        raise ValueError(f"K={K} is not a multiple of 16")
+
+
+def _fp8_act(h, K: int):
+    """(group size, sign_in, sign_out) of an optional Hadamard rotation."""
+    _fp8_width(K)
+    if h is None:
+        return 0, None, None
+    _hadamard_arg(h)
+    if K % h.g:
+        raise ValueError(f"K={K} is not a multiple of g={h.g}")
+    return h.g, h.sign_in, h.sign_out
+
+
+def _float_dtype(dtype, name: str):
+    if dtype not in _FLOAT:
+        raise ValueError(f"{name} {dtype} is not float32/float16/bfloat16")
+
+
+def w8a8_quantize_fp8(x: torch.Tensor, h: Optional[Hadamard] = None):
+    """Rows of x (..., K) to block-scaled fp8, rotated by h first if given.  Returns
+    (codes float8_e4m3fn (M, K), scales float32 (ceil(K/128), M): one per row and 128
+    k, k-block-major).  K % 16 == 0.  Scales held as (M, ceil(K/128)) elsewhere are
+    these transposed."""
+    x2 = _as_2d(_need(x, "x", contiguous=False))
+    M, K = x2.shape
+    dt = _dt(x2)
+    g, si, so = _fp8_act(h, K)
+    _same_device(x2, sign_in=si, sign_out=so)
+    dev = x2.device
+    codes = torch.empty((M, K), dtype=_E4M3, device=dev)
+    scales = torch.empty((_fp8_blocks(K), M), dtype=torch.float32, device=dev)
+    _call("w8a8_quantize_fp8", dev, _ptr(x2), dt, M, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(codes),
+          _ptr(scales))
+    return codes, scales
+
+
+def w8a8_quantize_weights_fp8(w: torch.Tensor, h: Optional[Hadamard] = None):
+    """Weights (N, K), or (E, N, K) of E experts, to block-scaled fp8 with one scale per
+    128 x 128, rotated along k by h first if given: (codes float8_e4m3fn like w, scales
+    float32 (.., ceil(N/128), ceil(K/128))).  K % 16 == 0.  A gated layer's gates and
+    ups, F each, keep blocks of their own if F % 128 == 0."""
+    _need(w, "w", contiguous=False)
+    dt = _dt(w)
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected (N, K) or (E, N, K)")
+    N, K = w.shape[-2:]
+    E, se = (w.shape[0], w.stride(0)) if w.dim() == 3 else (1, 0)
+    g, si, so = _fp8_act(h, K)
+    _same_device(w, sign_in=si, sign_out=so)
+    dev = w.device
+    codes = torch.empty(w.shape, dtype=_E4M3, device=dev)
+    scales = torch.empty((*w.shape[:-2], _fp8_blocks(N), _fp8_blocks(K)), dtype=torch.float32, device=dev)
+    _call("w8a8_quantize_weights_fp8", dev, _ptr(w), dt, E, N, K, se, w.stride(-2), w.stride(-1), g, _ptr(si), _ptr(so),
+          _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def w8a8_dequantize_fp8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values (M, K) that the codes and scales of rows stand for."""
+    M, K = _fp8_rows(codes, scales)
+    _float_dtype(dtype, "dtype")
+    _same_device(codes, scales=scales)
+    dev = codes.device
+    out = torch.empty((M, K), dtype=dtype, device=dev)
+    _call("w8a8_dequantize_fp8", dev, _ptr(codes), _ptr(scales), M, K, _ptr(out), _DT[dtype])
+    return out
+
+
+def w8a8_dequantize_weights_fp8(codes: torch.Tensor, scales: torch.Tensor,
+                                dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values that the codes and scales of weights (N, K) or (E, N, K) stand for."""
+    lead = 1 if isinstance(codes, torch.Tensor) and codes.dim() == 3 else 0
+    N, K = _fp8_weights(codes, scales, "codes", "scales", lead)
+    _float_dtype(dtype, "dtype")
+    _same_device(codes, scales=scales)
+    dev = codes.device
+    out = torch.empty(codes.shape, dtype=dtype, device=dev)
+    _call("w8a8_dequantize_weights_fp8", dev, _ptr(codes), _ptr(scales), codes.shape[0] if lead else 1, N, K, _ptr(out),
+          _DT[dtype])
+    return out
+
+
+def w8a8_gemm_fp8_plan(rows: int, K: int, N: int, experts: int = 0, gated: bool = False) -> str:
+    """Name of the kernel an fp8 product of `rows` rows takes (experts = 0: dense; 16-bit outputs)."""
+    k = ctypes.c_int(-1)
+    _check(lib().w8a8_gemm_fp8_plan(rows, K, N, experts, int(gated), ctypes.byref(k)), "w8a8_gemm_fp8_plan")
+    return FP8_KERNELS.get(k.value, "none")
+
+
+def w8a8_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                  bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The fp8 product: (M, N) from quantized rows and weights (N, K)."""
+    M, K = _fp8_rows(codes, scales)
+    N, Kw = _fp8_weights(w_codes, w_scales, "w_codes", "w_scales")
+    if Kw != K:
+        raise ValueError(f"w_codes has shape {tuple(w_codes.shape)}, expected (N, {K})")
+    if bias is not None:
+        _need(bias, "bias", (N,), _FLOAT)
+    _float_dtype(out_dtype, "out_dtype")
+    _same_device(codes, scales=scales, w_codes=w_codes, w_scales=w_scales, bias=bias)
+    dev = codes.device
+    out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _call("w8a8_gemm_fp8", dev, _ptr(codes), _ptr(scales), M, K, _ptr(w_codes), _ptr(w_scales), N, _ptr(bias),
+          _dt(bias) if bias is not None else 0, _ptr(out), _DT[out_dtype])
+    return out
+
+
+def w8a8_linear_fp8_workspace_size(M: int, K: int) -> int:
+    return int(lib().w8a8_linear_fp8_workspace_size(M, K))
+
+
+def w8a8_linear_fp8(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, h: Optional[Hadamard] = None,
+                    bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The linear layer on block-scaled fp8: x (..., K) is quantized (rotated by h first
+    if given) and multiplied by weights (N, K)."""
+    lead = _need(x, "x", contiguous=False).shape[:-1]
+    x2 = _as_2d(x)
+    M, K = x2.shape
+    dt = _dt(x2)
+    g, si, so = _fp8_act(h, K)
+    N, Kw = _fp8_weights(w_codes, w_scales, "w_codes", "w_scales")
+    if Kw != K:
+        raise ValueError(f"w_codes has shape {tuple(w_codes.shape)}, expected (N, {K})")
+    if bias is not None:
+        _need(bias, "bias", (N,), (x2.dtype,))
+    out_dtype = out_dtype or (out.dtype if out is not None else x2.dtype)
+    _float_dtype(out_dtype, "out_dtype")
+    if out is not None:
+        _need(out, "out", (M, N), (out_dtype,))
+    _same_device(x2, sign_in=si, sign_out=so, w_codes=w_codes, w_scales=w_scales, bias=bias, out=out,
+                 workspace=workspace)
+    dev = x2.device
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    workspace = _workspace(workspace, w8a8_linear_fp8_workspace_size(M, K), dev)
+    _call("w8a8_linear_fp8", dev, _ptr(x2), dt, M, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(w_codes),
+          _ptr(w_scales), N, _ptr(bias), _ptr(out), _DT[out_dtype], _ptr(workspace), workspace.numel())
+    return out if len(lead) == 1 else out.view(*lead, N)
+
+
+def _fp8_grouped(codes, scales, w_codes, w_scales, offsets, rows, bias, gated=False):
+    """Validation shared by the grouped products; returns (M, K, E, N, R)."""
+    M, K = _fp8_rows(codes, scales)
+    N, Kw = _fp8_weights(w_codes, w_scales, "w_codes", "w_scales", 1)
+    E = w_codes.shape[0]
+    if Kw != K:
+        raise ValueError(f"w_codes has shape {tuple(w_codes.shape)}, expected (E, N, {K})")
+    if gated and N % 256:
+        raise ValueError(f"w_codes has {N} rows per expert: gates and ups come in blocks of 128")
+    _need(offsets, "offsets", (E + 1,), (torch.int32,))
+    R = M
+    if rows is not None:
+        _need(rows, "rows", dtypes=(torch.int32,))
+        if rows.dim() != 1:
+            raise ValueError(f"rows has shape {tuple(rows.shape)}, expected (R,)")
+        R = rows.shape[0]
+    if bias is not None:
+        _need(bias, "bias", (E, N), _FLOAT)
+    _same_device(codes, scales=scales, w_codes=w_codes, w_scales=w_scales, offsets=offsets, rows=rows, bias=bias)
+    return M, K, E, N, R
+
+
+def w8a8_grouped_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                          offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                          bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """fp8 products grouped by expert: sorted row i (of expert e's offsets[e] ..
+    offsets[e + 1] - 1; int32 (E + 1,) on the device) is row rows[i] of codes (rows
+    None: row i) and meets expert e's weights (E, N, K).  Returns (R, N); rows before
+    offsets[0] and from offsets[E] on are zeros."""
+    M, K, E, N, R = _fp8_grouped(codes, scales, w_codes, w_scales, offsets, rows, bias)
+    _float_dtype(out_dtype, "out_dtype")
+    dev = codes.device
+    out = torch.empty((R, N), dtype=out_dtype, device=dev)
+    _call("w8a8_grouped_gemm_fp8", dev, _ptr(codes), _ptr(scales), M, K, _ptr(w_codes), _ptr(w_scales), E, N,
+          _ptr(offsets), _ptr(rows), R, _ptr(bias), _dt(bias) if bias is not None else 0, _ptr(out), _DT[out_dtype])
+    return out
+
+
+def w8a8_grouped_gated_fp8(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                           offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None):
+    """The grouped product with weights (E, 2 F, K), F gates then F ups (F % 128 == 0):
+    silu(gate) * up as quantized rows, (codes (R, F), scales (F/128, R))."""
+    M, K, E, N, R = _fp8_grouped(codes, scales, w_codes, w_scales, offsets, rows, bias, True)
+    dev = codes.device
+    out_codes = torch.empty((R, N // 2), dtype=_E4M3, device=dev)
+    out_scales = torch.empty((N // 256, R), dtype=torch.float32, device=dev)
+    _call("w8a8_grouped_gated_fp8", dev, _ptr(codes), _ptr(scales), M, K, _ptr(w_codes), _ptr(w_scales), E, N,
+          _ptr(offsets), _ptr(rows), R, _ptr(bias), _dt(bias) if bias is not None else 0, _ptr(out_codes),
+          _ptr(out_scales))
+    return out_codes, out_scales
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(E: int, top_k: int, scores, bias, groups, top_groups, group_best, renormalize, scale):
+    """Checks and arguments of routing by scores; top_groups None: all."""
+    if scores not in SCORES:
+        raise ValueError(f"scores {scores!r}: softmax or sigmoid")
+    top_groups = groups if top_groups is None else top_groups
+    if groups < 1 or E % groups:
+        raise ValueError(f"{groups} groups of {E} experts")
+    if not 1 <= top_groups <= groups:
+        raise ValueError(f"top_groups={top_groups} of {groups} groups")
+    if not 1 <= top_k <= E // groups * top_groups:
+        raise ValueError(f"top_k={top_k} of {E // groups * top_groups} experts in the top groups")
+    if group_best not in (1, 2):
+        raise ValueError(f"group_best={group_best} is not 1 or 2")
+    if bias is not None:
+        _need(bias, "bias", (E,), (torch.float32,))
+    return SCORES[scores], _ptr(bias), groups, top_groups, group_best, int(bool(renormalize)), float(scale)
+
+
+def w4a4_route_experts_scored(logits: torch.Tensor, top_k: int, scores: str = "softmax",
+                              bias: Optional[torch.Tensor] = None, groups: int = 1, top_groups: Optional[int] = None,
+                              group_best: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """Routing of logits (T, E) by scores: the softmax over all experts or the sigmoid
+    of a logit.  Experts are chosen by score + bias (float32 (E,); balances the load),
+    and weighted by the score itself, over the chosen scores' sum if renormalize, times
+    scale.  With groups, equal runs of neighbouring experts, only the experts of the
+    top_groups of largest worth can be chosen: the largest choice value of a group
+    (group_best 1) or the sum of its two largest (2).  Ties go to the lower index;
+    NaN and -inf logits and choice values are never taken.  Returns what
+    w4a4_route_experts returns: (weights, experts, rows, pos, offsets)."""
+    _need(logits, "logits", contiguous=False)
+    dt = _dt(logits)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1 and logits.shape[0]):
+        raise ValueError(f"logits must be (T, E) with contiguous rows, got shape {tuple(logits.shape)}")
+    T, E = logits.shape
+    how = _scoring(E, top_k, scores, bias, groups, top_groups, group_best, renormalize, scale)
+    _same_device(logits, bias=bias)
+    dev = logits.device
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    experts = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    rows = torch.empty((T * top_k,), dtype=torch.int32, device=dev)
+    pos = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    need = int(lib().w4a4_route_experts_workspace_size(T, E))
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    _call("w4a4_route_experts_scored", dev, _ptr(logits), dt, T, logits.stride(0), E, top_k, *how, _ptr(weights),
+          _ptr(experts), _ptr(rows), _ptr(pos), _ptr(offsets), _ptr(ws), need)
+    return weights, experts, rows, pos, offsets
+
+
+def w8a8_experts_fp8_workspace_size(T: int, K: int, F: int, E: int, top_k: int, dtype: torch.dtype) -> int:
+    """Bytes for w8a8_experts_fp8; dtype is that of the experts' rows (rows_dtype, else x's)."""
+    return int(lib().w8a8_experts_fp8_workspace_size(T, K, F, E, top_k, _DT[dtype]))
+
+
+def w8a8_experts_fp8(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_codes: torch.Tensor,
+                     w13_scales: torch.Tensor, w2_codes: torch.Tensor, w2_scales: torch.Tensor,
+                     h: Optional[Hadamard] = None, scores: str = "softmax", bias: Optional[torch.Tensor] = None,
+                     groups: int = 1, top_groups: Optional[int] = None, group_best: int = 1, renormalize: bool = True,
+                     scale: float = 1.0, workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     rows_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """The expert layer on x (..., K) with router logits (T, E), on block-scaled fp8:
+    route (as w4a4_route_experts_scored), quantize (rotated by h first if given), gated
+    product with w13 (E, 2 F, K; F gates then F ups, F % 128 == 0), product with w2 (E,
+    K, F), weighted sum per token.  The experts' rows wait for the sum in rows_dtype:
+    x's (a 16-bit layer then rounds twice), or float32."""
+    lead = _need(x, "x", contiguous=False).shape[:-1]
+    x2 = _as_2d(x)
+    T, K = x2.shape
+    dt = _dt(x2)
+    g, si, so = _fp8_act(h, K)
+    N1, K1 = _fp8_weights(w13_codes, w13_scales, "w13_codes", "w13_scales", 1)
+    N2, F = _fp8_weights(w2_codes, w2_scales, "w2_codes", "w2_scales", 1)
+    E = w13_codes.shape[0]
+    if K1 != K or N1 != 2 * F or N2 != K or w2_codes.shape[0] != E:
+        raise ValueError(f"w13_codes {tuple(w13_codes.shape)} and w2_codes {tuple(w2_codes.shape)} must be "
+                         f"(E, 2 F, {K}) and (E, {K}, F)")
+    if F % 128:
+        raise ValueError(f"F={F} is not a multiple of 128")
+    _need(logits, "logits", (T, E), _FLOAT, contiguous=False)
+    if logits.stride(1) != 1 and E > 1 and T:
+        raise ValueError("logits must have contiguous rows")
+    how = _scoring(E, top_k, scores, bias, groups, top_groups, group_best, renormalize, scale)
+    if out is not None:
+        _need(out, "out", (T, K), (x2.dtype,))
+    rows_dtype = rows_dtype or x2.dtype
+    if rows_dtype not in (x2.dtype, torch.float32):
+        raise ValueError(f"rows_dtype {rows_dtype} is not {x2.dtype} or float32")
+    _same_device(x2, sign_in=si, sign_out=so, logits=logits, bias=bias, w13_codes=w13_codes, w13_scales=w13_scales,
+                 w2_codes=w2_codes, w2_scales=w2_scales, workspace=workspace, out=out)
+    dev = x2.device
+    if out is None:
+        out = torch.empty((T, K), dtype=x2.dtype, device=dev)
+    workspace = _workspace(workspace, w8a8_experts_fp8_workspace_size(T, K, F, E, top_k, rows_dtype), dev)
+    _call("w8a8_experts_fp8", dev, _ptr(x2), dt, T, K, x2.stride(0), x2.stride(1), g, _ptr(si), _ptr(so), _ptr(logits),
+          _DT[logits.dtype], logits.stride(0), E, top_k, *how, _ptr(w13_codes), _ptr(w13_scales), F, _ptr(w2_codes),
+          _ptr(w2_scales), _DT[rows_dtype], _ptr(out), _ptr(workspace), workspace.numel())
     return out if len(lead) == 1 else out.view(*lead, K)

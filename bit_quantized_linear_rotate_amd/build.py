@@ -10,7 +10,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a4.so")
 PROBE_LIB = os.path.join(HERE, "libw4a4_probe.so")
 SOURCES = ["api.hip", "rotate_quant.hip", "rq_row.hip", "rq_hadamard.hip", "rq_svdquant.hip", "gemm.hip",
-           "lowrank.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_experts.hip"]
+           "lowrank.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_experts.hip",
+           "fp8_quant.hip", "fp8_gemm.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -26,7 +27,8 @@ HIPCC_FLAGS = [
 # which cannot read accumulation registers)
 SOURCE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "rq_row.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "rq_hadamard.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+                "rq_hadamard.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:

@@ -11,6 +11,7 @@
 #include "../../include/w4a4.h"
 #include "kernels.hpp"
 #include "mx4.hpp"
+#include "fp8.hpp"
 
 using namespace w4a4;
 
@@ -246,10 +247,11 @@ size_t route_bytes(int64_t T, int E)
     return c > 1 ? (size_t)c * (size_t)E * 4 : 0;
 }
 
-// the expert layer's workspace, in order
+// an expert layer's workspace, in order
 struct ExpertsSpace {
     size_t hist, weights, experts, rows, pos, offsets, codes, scales, act_codes, act_scales, y, total;
-    ExpertsSpace(int64_t T, int64_t K, int64_t F, int E, int k, int dtype)
+    ExpertsSpace(int64_t T, int64_t K, int E, int k, int dtype, size_t codes_bytes, size_t scales_bytes,
+                 size_t act_codes_bytes, size_t act_scales_bytes)
     {
         const int64_t R = T * k;
         size_t at = 0;
@@ -264,14 +266,141 @@ struct ExpertsSpace {
         rows = take((size_t)R * 4);
         pos = take((size_t)R * 4);
         offsets = take((size_t)(E + 1) * 4);
-        codes = take(mx4_codes_bytes(T, K));
-        scales = take(mx4_scales_bytes(T, K));
-        act_codes = take(mx4_codes_bytes(R, F));
-        act_scales = take(mx4_scales_bytes(R, F));
+        codes = take(codes_bytes);
+        scales = take(scales_bytes);
+        act_codes = take(act_codes_bytes);
+        act_scales = take(act_scales_bytes);
         y = take((size_t)R * (size_t)K * dsize(dtype));
         total = at;
     }
 };
+ExpertsSpace experts_mx4_space(int64_t T, int64_t K, int64_t F, int E, int k, int dtype)
+{
+    const int64_t R = T * k;
+    return ExpertsSpace(T, K, E, k, dtype, mx4_codes_bytes(T, K), mx4_scales_bytes(T, K), mx4_codes_bytes(R, F),
+                        mx4_scales_bytes(R, F));
+}
+
+// ---- block-scaled fp8 arguments --------------------------------------------
+constexpr int64_t kFp8MaxK = (int64_t)1 << 22;       // 256 rows of codes span at most 1 GB
+constexpr int64_t kFp8MaxRows = (int64_t)1 << 28;
+constexpr int kFp8MaxExperts = 16384;                // a grid of their row tiles stays below 2^16
+
+int fp8_shape(int64_t rows, int64_t K, const char* what)
+{
+    if (rows < 0 || K < 0) return fail(W4A4_INVALID, "negative size (%s)", what);
+    if (K % 16) return fail(W4A4_INVALID, "K=%lld is not a multiple of 16 (%s)", (long long)K, what);
+    if (rows > 0 && K == 0) return fail(W4A4_INVALID, "K=0 with rows (%s)", what);
+    if (K > kFp8MaxK || rows > kFp8MaxRows)
+        return fail(W4A4_UNSUPPORTED, "%lld rows of %lld values: at most 2^28 and 2^22 (%s)", (long long)rows, (long long)K,
+                    what);
+    return W4A4_OK;
+}
+
+int fp8_operand(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, const char* what)
+{
+    int rc = fp8_shape(rows, K, what);
+    if (rc) return rc;
+    if (rows > 0 && (!codes || !scales)) return fail(W4A4_INVALID, "codes/scales is NULL (%s)", what);
+    if ((uintptr_t)codes % 16 || (uintptr_t)scales % 4)
+        return fail(W4A4_UNSUPPORTED, "codes must be 16-byte and scales 4-byte aligned (%s)", what);
+    return W4A4_OK;
+}
+
+size_t fp8_codes_bytes(int64_t rows, int64_t K) { return rows > 0 && K > 0 ? (size_t)rows * (size_t)K : 0; }
+size_t fp8_scales_bytes(int64_t rows, int64_t K)
+{
+    return rows > 0 && K > 0 ? (size_t)fp8_blocks(K) * (size_t)rows * 4 : 0;
+}
+
+int fp8_quant_validate(const void* x, int x_dtype, int64_t E, int64_t M, int64_t K, int64_t sm, int64_t sk, int32_t g,
+                       const int8_t* sign_in, const int8_t* sign_out)
+{
+    int rc = check_activation(x, x_dtype, E ? M : 0, K, sm, sk, false);
+    if (rc) return rc;
+    rc = fp8_shape(M, K, "x");
+    if (rc) return rc;
+    // sixteen rows of 256 values per workgroup of 256: less than 2^32 threads
+    if ((M / 16 + 1) * (K / 256 + 1) * (E > 1 ? E : 1) >= (int64_t)1 << 24)
+        return fail(W4A4_UNSUPPORTED, "%lld x %lld values are too many for one call", (long long)M, (long long)K);
+    if (g < 0) return fail(W4A4_INVALID, "group size g=%d", g);
+    if (g == 0) return W4A4_OK;
+    if (!pow2_g(g)) return fail(W4A4_UNSUPPORTED, "g=%d is not a power of two in [16, 256]", g);
+    if (K % g) return fail(W4A4_INVALID, "K=%lld is not a multiple of g=%d", (long long)K, g);
+    if ((uintptr_t)sign_in % 8 || (uintptr_t)sign_out % 8)
+        return fail(W4A4_UNSUPPORTED, "sign_in and sign_out must be 8-byte aligned");
+    return W4A4_OK;
+}
+
+int fp8_gemm_validate(const Fp8GemmArgs& a)
+{
+    int rc = fp8_operand(a.a, a.sa, a.M, a.K, "activations");
+    if (rc) return rc;
+    if (a.N < 0) return fail(W4A4_INVALID, "negative size");
+    rc = fp8_operand(a.b, a.sb, a.N, a.K, "weights");
+    if (rc) return rc;
+    if (fp8_scales_bytes(a.M, a.K) > (size_t)1 << 31)
+        return fail(W4A4_UNSUPPORTED, "activations with more than 2^31 bytes of scales");
+    const bool gated = a.out_codes || a.out_scales;
+    if ((!gated && !dtype_ok(a.out_dtype)) || (a.bias && !dtype_ok(a.bias_dtype)))
+        return fail(W4A4_UNSUPPORTED, "unknown dtype code");
+    const int64_t rows = a.E ? a.R : a.M;
+    if (rows > 0 && a.N > 0 && !gated && !a.out) return fail(W4A4_INVALID, "out is NULL");
+    // tiles of 64 rows and 256 columns at the least: the grid stays below 2^31 threads
+    if ((rows / 64 + a.E + 1) * (a.N / 128 + 1) >= (int64_t)1 << 22)
+        return fail(W4A4_UNSUPPORTED, "an output of %lld x %lld is too large for one call", (long long)rows, (long long)a.N);
+    return W4A4_OK;
+}
+
+int fp8_grouped_validate(const Fp8GemmArgs& a)
+{
+    if (a.E < 1) return fail(W4A4_INVALID, "E=%d experts", a.E);
+    if (a.E > kFp8MaxExperts) return fail(W4A4_UNSUPPORTED, "E=%d experts: at most %d", a.E, kFp8MaxExperts);
+    if (a.R < 0) return fail(W4A4_INVALID, "negative size");
+    if (a.R >= (int64_t)1 << 31) return fail(W4A4_UNSUPPORTED, "%lld sorted rows: at most 2^31 - 1", (long long)a.R);
+    int rc = fp8_gemm_validate(a);
+    if (rc) return rc;
+    if (a.R > 0 && !a.offsets) return fail(W4A4_INVALID, "offsets is NULL");
+    if (!a.rows && a.M != a.R)
+        return fail(W4A4_INVALID, "%lld rows of codes for %lld sorted rows and no row index", (long long)a.M, (long long)a.R);
+    if (a.rows && a.M * a.K > (int64_t)1 << 31)
+        return fail(W4A4_UNSUPPORTED, "codes of more than 2^31 bytes behind a row index");
+    return W4A4_OK;
+}
+
+int fp8_gated_validate(const Fp8GemmArgs& a)
+{
+    if (a.N % (2 * kFp8Block))
+        return fail(W4A4_INVALID, "N=%lld: gates and ups come in blocks of 128, N in multiples of 256", (long long)a.N);
+    int rc = fp8_grouped_validate(a);
+    if (rc) return rc;
+    if (a.R > 0 && a.N > 0 && (!a.out_codes || !a.out_scales)) return fail(W4A4_INVALID, "out_codes/out_scales is NULL");
+    if ((uintptr_t)a.out_codes % 16 || (uintptr_t)a.out_scales % 4)
+        return fail(W4A4_UNSUPPORTED, "out_codes must be 16-byte and out_scales 4-byte aligned");
+    return W4A4_OK;
+}
+
+int scoring_validate(const RouteScoredArgs& a)
+{
+    const int rc = route_validate(a);
+    if (rc) return rc;
+    if (a.groups < 1 || a.E % a.groups) return fail(W4A4_INVALID, "%d groups of E=%d experts", a.groups, a.E);
+    if (a.groups > kRouteMaxGroups) return fail(W4A4_UNSUPPORTED, "%d groups: at most %d", a.groups, kRouteMaxGroups);
+    if (a.top_groups < 1 || a.top_groups > a.groups)
+        return fail(W4A4_INVALID, "top_groups=%d of %d groups", a.top_groups, a.groups);
+    if (a.k > a.E / a.groups * a.top_groups)
+        return fail(W4A4_INVALID, "top_k=%d of %d experts in the top groups", a.k, a.E / a.groups * a.top_groups);
+    if (a.group_best != 1 && a.group_best != 2) return fail(W4A4_INVALID, "group_best=%d is not 1 or 2", a.group_best);
+    return W4A4_OK;
+}
+
+// the expert layer's workspace on fp8
+ExpertsSpace experts_fp8_space(int64_t T, int64_t K, int64_t F, int E, int k, int dtype)
+{
+    const int64_t R = T * k;
+    return ExpertsSpace(T, K, E, k, dtype, fp8_codes_bytes(T, K), fp8_scales_bytes(T, K), fp8_codes_bytes(R, F),
+                        fp8_scales_bytes(R, F));
+}
 
 // Scratch of w4a4_linear_noalloc: the codes, scales, low-rank activations
 // and (for very long K) int64 partial sums of one call.  Each GPU the library
@@ -1172,7 +1301,7 @@ int w4a4_combine_experts_to(const void* y, int dtype, int64_t R, int64_t N, cons
 size_t w4a4_experts_mx4_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k, int rows_dtype)
 {
     if (T <= 0 || K <= 0 || F <= 0 || E <= 0 || top_k <= 0 || !dtype_ok(rows_dtype)) return 0;
-    return ExpertsSpace(T, K, F, E, top_k, rows_dtype).total;
+    return experts_mx4_space(T, K, F, E, top_k, rows_dtype).total;
 }
 
 int w4a4_experts_mx4(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
@@ -1202,7 +1331,7 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
     if (T == 0) return W4A4_OK;
     if (T * top_k >= (int64_t)1 << 28)
         return fail(W4A4_UNSUPPORTED, "T top_k = %lld: at most 2^28 - 1", (long long)(T * top_k));
-    const ExpertsSpace at(T, K, F, E, top_k, rows_dtype);
+    const ExpertsSpace at = experts_mx4_space(T, K, F, E, top_k, rows_dtype);
     if (!workspace || workspace_bytes < at.total)
         return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, at.total);
     if ((uintptr_t)workspace % 16) return fail(W4A4_UNSUPPORTED, "the workspace must be 16-byte aligned");
@@ -1243,6 +1372,249 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
     if (e != hipSuccess) return hip_fail(e, "mx4 gated grouped gemm launch");
     e = launch_mx4_gemm(g2, st);
     if (e != hipSuccess) return hip_fail(e, "mx4 grouped gemm launch");
+    e = launch_combine(ca, st);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "combining launch");
+}
+
+// ---- block-scaled 8-bit floating point --------------------------------------
+
+int w8a8_quantize_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                      const int8_t* sign_in, const int8_t* sign_out, uint8_t* codes, float* scales, void* stream)
+{
+    int rc = fp8_quant_validate(x, x_dtype, 1, M, K, stride_m, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    rc = fp8_operand(codes, scales, M, K, "codes");
+    if (rc || M == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const Fp8QuantArgs a{x, x_dtype, M, K, stride_m, stride_k, g, sign_in, sign_out, codes, scales};
+    const hipError_t e = launch_fp8_quantize(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 quantizer launch");
+}
+
+int w8a8_quantize_weights_fp8(const void* w, int w_dtype, int64_t E, int64_t N, int64_t K, int64_t stride_e, int64_t stride_n,
+                              int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out, uint8_t* codes,
+                              float* scales, void* stream)
+{
+    if (E < 0 || stride_e < 0) return fail(W4A4_INVALID, "E=%lld matrices, stride %lld", (long long)E, (long long)stride_e);
+    if (E > 65535) return fail(W4A4_UNSUPPORTED, "E=%lld matrices: at most 65535", (long long)E);
+    int rc = fp8_quant_validate(w, w_dtype, E, N, K, stride_n, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    rc = fp8_operand(codes, scales, E ? N : 0, K, "codes");
+    if (rc || E == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    Fp8QuantArgs a{w, w_dtype, N, K, stride_n, stride_k, g, sign_in, sign_out, codes, scales};
+    a.E = E;
+    a.se = stride_e;
+    const hipError_t e = launch_fp8_quantize_weights(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 weight quantizer launch");
+}
+
+static int dequantize_fp8(const uint8_t* codes, const float* scales, int64_t E, int64_t M, int64_t K, void* out, int out_dtype,
+                          void* stream)
+{
+    int rc = fp8_operand(codes, scales, M, K, "codes");
+    if (rc) return rc;
+    if (!dtype_ok(out_dtype)) return fail(W4A4_UNSUPPORTED, "unknown dtype code %d", out_dtype);
+    if (M > 0 && !out) return fail(W4A4_INVALID, "out is NULL");
+    if ((uintptr_t)out % 16) return fail(W4A4_UNSUPPORTED, "out must be 16-byte aligned");
+    if (M == 0) return W4A4_OK;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_fp8_dequantize(codes, scales, E, M, K, out, out_dtype, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 dequantizer launch");
+}
+
+int w8a8_dequantize_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K, void* out, int out_dtype, void* stream)
+{
+    return dequantize_fp8(codes, scales, 0, M, K, out, out_dtype, stream);
+}
+
+int w8a8_dequantize_weights_fp8(const uint8_t* codes, const float* scales, int64_t E, int64_t N, int64_t K, void* out,
+                                int out_dtype, void* stream)
+{
+    if (E < 0 || E > 65535) return fail(E < 0 ? W4A4_INVALID : W4A4_UNSUPPORTED, "E=%lld matrices", (long long)E);
+    return dequantize_fp8(codes, scales, E ? E : 1, E ? N : 0, K, out, out_dtype, stream);
+}
+
+int w8a8_gemm_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K, const uint8_t* w_codes,
+                  const float* w_scales, int64_t N, const void* bias, int bias_dtype, void* out, int out_dtype, void* stream)
+{
+    const Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    int rc = fp8_gemm_validate(a);
+    if (rc || M == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_fp8_gemm(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 gemm launch");
+}
+
+int w8a8_gemm_fp8_plan(int64_t rows, int64_t K, int64_t N, int32_t E, int32_t gated, int* kernel)
+{
+    if (!kernel) return fail(W4A4_INVALID, "kernel is NULL");
+    if (E < 0 || (gated && !E)) return fail(W4A4_INVALID, "E=%d experts", E);
+    int rc = fp8_shape(rows, K, "activations");
+    if (rc) return rc;
+    rc = fp8_shape(N, K, "weights");
+    if (rc) return rc;
+    Fp8GemmArgs a{nullptr, nullptr, rows, K, N, nullptr, nullptr, nullptr, 0, nullptr, W4A4_BF16};
+    a.E = E;
+    a.R = rows;
+    if (gated) a.out_codes = (uint8_t*)16;
+    *kernel = rows == 0 || N == 0 ? -1 : fp8_gemm_path(a);
+    return W4A4_OK;
+}
+
+size_t w8a8_linear_fp8_workspace_size(int64_t M, int64_t K)
+{
+    return M > 0 && K > 0 ? align256(fp8_codes_bytes(M, K)) + align256(fp8_scales_bytes(M, K)) : 0;
+}
+
+int w8a8_linear_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                    const int8_t* sign_in, const int8_t* sign_out, const uint8_t* w_codes, const float* w_scales, int64_t N,
+                    const void* bias, void* out, int out_dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = fp8_quant_validate(x, x_dtype, 1, M, K, stride_m, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    if (N < 0) return fail(W4A4_INVALID, "negative size");
+    if (M == 0 || N == 0) return W4A4_OK;
+    if (!workspace || workspace_bytes < w8a8_linear_fp8_workspace_size(M, K))
+        return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, w8a8_linear_fp8_workspace_size(M, K));
+    uint8_t* codes = (uint8_t*)workspace;
+    float* scales = (float*)(codes + align256(fp8_codes_bytes(M, K)));
+    const Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, x_dtype, out, out_dtype};
+    rc = fp8_gemm_validate(a);
+    if (rc) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    hipStream_t st = (hipStream_t)stream;
+    const Fp8QuantArgs qa{x, x_dtype, M, K, stride_m, stride_k, g, sign_in, sign_out, codes, scales};
+    hipError_t e = launch_fp8_quantize(qa, st);
+    if (e != hipSuccess) return hip_fail(e, "fp8 quantizer launch");
+    e = launch_fp8_gemm(a, st);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 gemm launch");
+}
+
+int w8a8_grouped_gemm_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K, const uint8_t* w_codes,
+                          const float* w_scales, int32_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
+                          int64_t R, const void* bias, int bias_dtype, void* out, int out_dtype, void* stream)
+{
+    Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    a.E = E;
+    a.R = R;
+    a.offsets = offsets;
+    a.rows = rows;
+    int rc = fp8_grouped_validate(a);
+    if (rc || R == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_fp8_gemm(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 grouped gemm launch");
+}
+
+int w8a8_grouped_gated_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K, const uint8_t* w_codes,
+                           const float* w_scales, int32_t E, int64_t N, const int32_t* offsets, const int32_t* rows,
+                           int64_t R, const void* bias, int bias_dtype, uint8_t* out_codes, float* out_scales, void* stream)
+{
+    Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, nullptr, W4A4_BF16};
+    a.E = E;
+    a.R = R;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.out_codes = out_codes;
+    a.out_scales = out_scales;
+    if (R > 0 && N > 0 && (!out_codes || !out_scales)) return fail(W4A4_INVALID, "out_codes/out_scales is NULL");
+    int rc = fp8_gated_validate(a);
+    if (rc || R == 0 || N == 0) return rc;
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_fp8_gemm(a, (hipStream_t)stream);
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "fp8 gated grouped gemm launch");
+}
+
+int w4a4_route_experts_scored(const void* logits, int dtype, int64_t T, int64_t stride, int32_t E, int32_t top_k,
+                              int32_t sigmoid, const float* bias, int32_t groups, int32_t top_groups, int32_t group_best,
+                              int32_t renormalize, float scale, float* weights, int32_t* experts, int32_t* rows,
+                              int32_t* pos, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const RouteScoredArgs a{{logits, dtype, T, stride, E, top_k, renormalize, weights, experts, rows, pos, offsets,
+                             (int32_t*)workspace}, sigmoid, bias, groups, top_groups, group_best, scale};
+    int rc = scoring_validate(a);
+    if (rc) return rc;
+    const size_t need = w4a4_route_experts_workspace_size(T, E);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+    rc = device_check();
+    if (rc) return rc;
+    const hipError_t e = launch_route_scored(a, (hipStream_t)stream);   // (T = 0: the offsets are still written)
+    return e == hipSuccess ? W4A4_OK : hip_fail(e, "routing launch");
+}
+
+size_t w8a8_experts_fp8_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k, int rows_dtype)
+{
+    if (T <= 0 || K <= 0 || F <= 0 || E <= 0 || top_k <= 0 || !dtype_ok(rows_dtype)) return 0;
+    return experts_fp8_space(T, K, F, E, top_k, rows_dtype).total;
+}
+
+int w8a8_experts_fp8(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m, int64_t stride_k, int32_t g,
+                     const int8_t* sign_in, const int8_t* sign_out, const void* logits, int logits_dtype,
+                     int64_t logits_stride, int32_t E, int32_t top_k, int32_t sigmoid, const float* bias, int32_t groups,
+                     int32_t top_groups, int32_t group_best, int32_t renormalize, float scale, const uint8_t* w13_codes,
+                     const float* w13_scales, int64_t F, const uint8_t* w2_codes, const float* w2_scales, int rows_dtype,
+                     void* out, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = fp8_quant_validate(x, x_dtype, 1, T, K, stride_m, stride_k, g, sign_in, sign_out);
+    if (rc) return rc;
+    if (rows_dtype != x_dtype && rows_dtype != W4A4_F32)
+        return fail(W4A4_UNSUPPORTED, "rows dtype code %d: x's or fp32", rows_dtype);
+    if (F < 1 || F % kFp8Block) return fail(W4A4_INVALID, "F=%lld is not a positive multiple of 128", (long long)F);
+    if (E < 1 || top_k < 1 || top_k > E) return fail(W4A4_INVALID, "top_k=%d of E=%d experts", top_k, E);
+    if (T == 0) return W4A4_OK;
+    if (T * top_k >= (int64_t)1 << 28)
+        return fail(W4A4_UNSUPPORTED, "T top_k = %lld: at most 2^28 - 1", (long long)(T * top_k));
+    const ExpertsSpace at = experts_fp8_space(T, K, F, E, top_k, rows_dtype);
+    if (!workspace || workspace_bytes < at.total)
+        return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, at.total);
+    if ((uintptr_t)workspace % 16) return fail(W4A4_UNSUPPORTED, "the workspace must be 16-byte aligned");
+    if (!out) return fail(W4A4_INVALID, "out is NULL");
+    uint8_t* ws = (uint8_t*)workspace;
+    float* weights = (float*)(ws + at.weights);
+    int32_t *rows = (int32_t*)(ws + at.rows), *pos = (int32_t*)(ws + at.pos), *offsets = (int32_t*)(ws + at.offsets);
+    const int64_t R = T * top_k;
+    const RouteScoredArgs ra{{logits, logits_dtype, T, logits_stride, E, top_k, renormalize, weights,
+                              (int32_t*)(ws + at.experts), rows, pos, offsets, (int32_t*)(ws + at.hist)},
+                             sigmoid, bias, groups, top_groups, group_best, scale};
+    rc = scoring_validate(ra);
+    if (rc) return rc;
+    const Fp8QuantArgs qa{x, x_dtype, T, K, stride_m, stride_k, g, sign_in, sign_out, ws + at.codes, (float*)(ws + at.scales)};
+    Fp8GemmArgs g1{qa.codes, qa.scales, T, K, 2 * F, w13_codes, w13_scales, nullptr, 0, nullptr, W4A4_BF16};
+    g1.E = E;
+    g1.R = R;
+    g1.offsets = offsets;
+    g1.rows = rows;
+    g1.out_codes = ws + at.act_codes;
+    g1.out_scales = (float*)(ws + at.act_scales);
+    rc = fp8_gated_validate(g1);
+    if (rc) return rc;
+    Fp8GemmArgs g2{g1.out_codes, g1.out_scales, R, F, K, w2_codes, w2_scales, nullptr, 0, ws + at.y, rows_dtype};
+    g2.E = E;
+    g2.R = R;
+    g2.offsets = offsets;
+    rc = fp8_grouped_validate(g2);
+    if (rc) return rc;
+    const CombineArgs ca{ws + at.y, rows_dtype, R, T, K, top_k, pos, weights, out, x_dtype};
+    rc = device_check();
+    if (rc) return rc;
+    hipStream_t st = (hipStream_t)stream;
+    hipError_t e = launch_route_scored(ra, st);
+    if (e != hipSuccess) return hip_fail(e, "routing launch");
+    e = launch_fp8_quantize(qa, st);
+    if (e != hipSuccess) return hip_fail(e, "fp8 quantizer launch");
+    e = launch_fp8_gemm(g1, st);
+    if (e != hipSuccess) return hip_fail(e, "fp8 gated grouped gemm launch");
+    e = launch_fp8_gemm(g2, st);
+    if (e != hipSuccess) return hip_fail(e, "fp8 grouped gemm launch");
     e = launch_combine(ca, st);
     return e == hipSuccess ? W4A4_OK : hip_fail(e, "combining launch");
 }

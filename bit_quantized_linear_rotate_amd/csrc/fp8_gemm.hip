@@ -1,0 +1,775 @@
+// The block-scaled fp8 product
+//   out[m][n] = sum_b sa[b][m] sw[n / 128][b] (sum_{k in block b} a[m][k] w[n][k]) (+ bias[n])
+// on gfx950's f8f6f4 matrix cores, dense and grouped by expert.
+//
+// Mathematics.  v_mfma_f32_16x16x128_f8f6f4 multiplies 16 x 128 by 128 x 16 e4m3
+// values: one block of k.  It starts from zero, and its fp32 result joins the
+// accumulators with one fma per output, times the product of the two scales.  The
+// weights are the first operand, so a lane (j, q) ends with columns 4q .. 4q + 3 of
+// one row j of a 16 x 16 tile, and a single factor serves all of a row's columns
+// that share a weight block.  A lane supplies 32 k of one row; which 32 is free as
+// long as both operands agree.
+//
+// Precision.  The fp8 matrix core adds the products of eight neighbouring k in fixed
+// point, 2^-13 of the largest of them the last place (measured: a product of 2^-14
+// beside one of 1 is lost inside such a group, kept outside it), and the groups in
+// fp32.  For random rows that is 1.5e-5 of a sum, a hundredth of the rounding to 16
+// bits and less of that to codes; where the output is fp32 it would be the largest
+// error of all, so those products convert the codes (exactly) to fp16, whose matrix
+// core (16x16x32, half the rate) is 1e-8 off.
+#include "common.hpp"
+#include "fp8.hpp"
+#include "fp8_codes.hpp"
+#include "grouped.hpp"
+
+namespace w4a4 {
+
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+// 16 x 16 outputs of one block of 128 k, from zero
+__device__ __forceinline__ v4f fp8_mfma(v8i w, v8i a)
+{
+    const v4f z = {0.f, 0.f, 0.f, 0.f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, z, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ v8i join(v4i lo, v4i hi)
+{
+    return (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+// The lane's 32 codes as fp16, four operands of the 16x16x32 instruction
+__device__ __forceinline__ void fp8_to_f16(v8i c, v8h (&h)[4])
+{
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const v2h p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t], 1.0f, false);
+        const v2h p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t], 1.0f, true);
+        const v2h p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t + 1], 1.0f, false);
+        const v2h p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t + 1], 1.0f, true);
+        h[t] = (v8h){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+    }
+}
+__device__ __forceinline__ v4f f16_mfma(const v8h (&w)[4], const v8h (&a)[4])
+{
+    v4f d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], a[t], d, 0, 0, 0);
+    return d;
+}
+
+// Zeros for the sorted rows that no expert owns (before offsets[0] and from
+// offsets[E] on), spread over the workgroups that have no tile.
+__device__ __forceinline__ void fp8_zero_rows(const Fp8GemmArgs& a, int64_t part, int64_t parts)
+{
+    const int64_t first = mx_offset(a, 0), from = max(mx_offset(a, a.E), first), rows = first + a.R - from;
+    const int64_t start = part * blockDim.x + threadIdx.x, step = parts * blockDim.x;
+    auto at = [&](int64_t i, int64_t n) { return i < first * n ? i : i + (from - first) * n; };
+    if (a.out_codes) {
+        const int64_t F = a.N / 2, blocks = F / kFp8Block;
+        for (int64_t i = start; i < rows * F; i += step) a.out_codes[at(i, F)] = 0;
+        for (int64_t i = start; i < rows * blocks; i += step) a.out_scales[i / rows * a.R + at(i % rows, 1)] = 0.0f;
+    } else {
+        const int64_t wide = a.N * (a.out_dtype == F32 ? 2 : 1);
+        uint16_t* o = (uint16_t*)a.out;
+        for (int64_t i = start; i < rows * wide; i += step) o[at(i, wide)] = 0;
+    }
+}
+
+// ---- the skinny kernel -------------------------------------------------------
+// Few rows: the weights are the cost, read once, straight into registers.  A
+// workgroup of eight waves takes 16 MT rows; KW of its waves share the K steps of
+// one group of 16 NT columns, 8 / KW groups lie side by side (gated: a group is 16
+// gates and their 16 ups, KW = 1, and the eight groups are one block of 128
+// results).  Partial sums meet in LDS and are added in wave order.
+constexpr int kSkinnyWaves = 8;
+template <int MT, int NT, int KW, bool GROUPED, bool GATED, bool HALF>
+__global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
+{
+    static_assert(!GATED || (NT == 2 && KW == 1), "a block of results per workgroup");
+    constexpr int W = kSkinnyWaves, CG = W / KW;
+    constexpr int COLS = GATED ? 16 : 16 * NT;   // results of a column group
+    __shared__ float part[W][MT][NT][16][17];    // [wave][row tile][column tile][row][column]
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int kw = wave % KW, cg = wave / KW;
+    const int j = lane & 15, q = lane >> 4;
+    const int64_t K = a.K, N = a.N, F = N >> 1;
+    const int64_t n = GATED ? F : N;             // results of a row
+    const int nsteps = (int)fp8_blocks(K);
+    int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    int rows, e = 0;
+    if constexpr (GROUPED) {
+        MxRows r;
+        const int64_t total = mx_find<16 * MT, true>(a, blockIdx.y, r);
+        if (r.e < 0) {
+            fp8_zero_rows(a, (int64_t)(blockIdx.y - total) * gridDim.x + blockIdx.x, (int64_t)(gridDim.y - total) * gridDim.x);
+            return;
+        }
+        const int m = (int)(blockIdx.y - r.before);
+        e = r.e;
+        m0 = r.m0 + (int64_t)m * (16 * MT);
+        rows = min(r.rows - m * 16 * MT, 16 * MT);
+    } else {
+        rows = (int)min(a.M - m0, (int64_t)(16 * MT));
+    }
+    const uint8_t* wb = a.b + (int64_t)e * N * K;
+    const float* wsb = a.sb + (int64_t)e * fp8_blocks(N) * nsteps;
+    const int64_t first = ((int64_t)blockIdx.x * CG + cg) * COLS;   // the group's first result
+    // this lane's weight columns and rows (clamped: what they give is not stored)
+    int64_t col[NT], src[MT];
+    const float* ws[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int64_t c = first + (GATED ? 0 : nt * 16);
+        const int64_t up = GATED ? nt * F : 0;
+        col[nt] = min(c + j, n - 1) + up;
+        ws[nt] = wsb + (min(c, n - 1) + up) / kFp8Block * nsteps;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int i = 16 * mt + j;
+        int64_t s = m0 + (i < rows ? i : rows - 1);
+        bool ok = true;
+        if (GROUPED && a.rows) {
+            s = a.rows[s];
+            ok = s >= 0 && s < a.M;
+        }
+        src[mt] = ok ? s : -1;
+    }
+    v4f acc[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = (v4f){0.f, 0.f, 0.f, 0.f};
+    constexpr int U = NT * MT > 4 ? 1 : 2;     // steps in flight
+    for (int s0 = kw; s0 < nsteps; s0 += KW * U) {
+        v4i fb[U][NT][2], fa[U][MT][2];
+        float sw[U][NT], sa[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + KW * u;
+            const bool in = s < nsteps;
+            const int64_t k = (int64_t)s * kFp8Block + 32 * q;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint8_t* p = wb + col[nt] * K + k;
+                fb[u][nt][0] = in && k < K ? *(const v4i*)p : (v4i){0, 0, 0, 0};
+                fb[u][nt][1] = in && k + 16 < K ? *(const v4i*)(p + 16) : (v4i){0, 0, 0, 0};
+                sw[u][nt] = in ? ws[nt][s] : 0.0f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const bool ok = in && src[mt] >= 0;
+                const uint8_t* p = a.a + src[mt] * K + k;
+                fa[u][mt][0] = ok && k < K ? *(const v4i*)p : (v4i){0, 0, 0, 0};
+                fa[u][mt][1] = ok && k + 16 < K ? *(const v4i*)(p + 16) : (v4i){0, 0, 0, 0};
+                sa[u][mt] = ok ? a.sa[(int64_t)s * a.M + src[mt]] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    v4f p;
+                    if constexpr (HALF) {
+                        v8h hb[4], ha[4];
+                        fp8_to_f16(join(fb[u][nt][0], fb[u][nt][1]), hb);
+                        fp8_to_f16(join(fa[u][mt][0], fa[u][mt][1]), ha);
+                        p = f16_mfma(hb, ha);
+                    } else {
+                        p = fp8_mfma(join(fb[u][nt][0], fb[u][nt][1]), join(fa[u][mt][0], fa[u][mt][1]));
+                    }
+                    const float f = mul_rn(sa[u][mt], sw[u][nt]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[mt][nt][r] = __builtin_fmaf(p[r], f, acc[mt][nt][r]);
+                }
+    }
+    // lane (j, q): row j of the row tile, columns 4q .. 4q + 3 of the column tile
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) part[wave][mt][nt][j][4 * q + r] = acc[mt][nt][r];
+    __syncthreads();
+    const int waves = nsteps < KW ? nsteps : KW;   // those that had a step
+    auto sum = [&](int g, int mt, int nt, int row, int c) {
+        float v = part[g * KW][mt][nt][row][c];
+        for (int w = 1; w < waves; ++w) v = add_rn(v, part[g * KW + w][mt][nt][row][c]);
+        return v;
+    };
+    if constexpr (GATED) {
+        // half a wave takes the 128 results of a row, four a lane
+        const int l = tid & 31;
+        const int64_t f0 = (int64_t)blockIdx.x * kFp8Block, f = f0 + 4 * l;
+        for (int row = tid >> 5; row < 16 * MT; row += 16) {
+            if (row >= rows) continue;   // (whole half waves)
+            const int mt = row >> 4;
+            float v[4];
+            uint32_t m = 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float g = sum(l >> 2, mt, 0, row & 15, 4 * (l & 3) + r), u = sum(l >> 2, mt, 1, row & 15, 4 * (l & 3) + r);
+                if (a.bias) {
+                    g = add_rn(g, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + f + r));
+                    u = add_rn(u, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + F + f + r));
+                }
+                v[r] = mx_gated(g, u);
+                m = max(m, __float_as_uint(v[r]) & 0x7fffffffu);
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+            const Fp8Block b = fp8_block(m);
+            *(uint32_t*)(a.out_codes + (m0 + row) * F + f) = fp8_codes4(b, v[0], v[1], v[2], v[3]);
+            if (l == 0) a.out_scales[(int64_t)blockIdx.x * a.R + m0 + row] = b.scale;
+        }
+    } else {
+        constexpr int WG = CG * COLS;
+        for (int i = tid; i < 16 * MT * WG; i += 512) {
+            const int row = i / WG, c = i % WG, g = c / COLS, nt = (c % COLS) >> 4;
+            const int64_t nn = (int64_t)blockIdx.x * WG + c;
+            if (nn < N && row < rows) {
+                float v = sum(g, row >> 4, nt, row & 15, c & 15);
+                if (a.bias) v = add_rn(v, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + nn));
+                store_any(a.out_dtype, a.out, (m0 + row) * N + nn, v);
+            }
+        }
+    }
+}
+
+// ---- the tile kernel ---------------------------------------------------------
+// The epilogue of a wave: rows row0 + 16 mt of the tile, sixteen consecutive
+// columns from n0 + c0 in this lane, as pieces of 16 bytes (the columns of a row
+// need not be aligned to them).  Range-checked buffer stores, so that every wave
+// issues the same number of them whatever the tile holds.  CUT: the piece that the
+// matrix's last column cuts goes out a value at a time.
+template <int ODT, int MT, bool BIAS, bool CUT>
+__device__ __forceinline__ void fp8_put(const Fp8GemmArgs& a, const v4f (&acc)[MT][4], int64_t m0, int row0, int rows,
+                                        int64_t n0, int c0, int e)
+{
+    constexpr int ESZ = ODT == F32 ? 4 : 2, PIECE = 16 / ESZ, P = 16 / PIECE;
+    const int64_t N = a.N;
+    const __amdgpu_buffer_rsrc_t ro =
+        mx_rsrc(mx_uniform((const uint8_t*)a.out + (m0 * N + n0) * ESZ), ((int64_t)rows * N - n0) * ESZ);
+    const uint32_t rstep = (uint32_t)(16 * N * ESZ), off = (uint32_t)((row0 * N + c0) * ESZ);
+    const int left = (int)min(N - n0, (int64_t)256) - c0;   // columns from this lane's first
+    float bv[1][16];
+    if constexpr (BIAS) mx_bias<1>(a, e, 0, N, n0 + c0, bv);
+    uint32_t at[P];   // (past the resource, and so with any mt rstep, where the piece is not whole)
+#pragma unroll
+    for (int p = 0; p < P; ++p) at[p] = PIECE * (p + 1) <= left ? off + PIECE * p * ESZ : kOut;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[i] = acc[mt][i >> 2][i & 3];
+            if constexpr (BIAS) v[i] = add_rn(v[i], bv[0][i]);
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            v4u w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (ODT == F32) w[i] = __float_as_uint(v[4 * p + i]);
+                else w[i] = mx_pack2<ODT>(v[8 * p + 2 * i], v[8 * p + 2 * i + 1]);
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(w, ro, (int)(at[p] + mt * rstep), 0, 0);
+        }
+        if constexpr (CUT) {
+            const int from = left / PIECE * PIECE;   // of these sixteen columns, up to `left`
+            if (row0 + 16 * mt < rows && left > 0 && from < 16) {
+                char* o = (char*)a.out + ((m0 + row0 + 16 * mt) * N + n0 + c0) * ESZ;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i >= from && i < left) store_any(ODT, o, i, v[i]);
+            }
+        }
+    }
+}
+
+template <int ODT, int MT>
+__device__ __forceinline__ void fp8_epilogue(const Fp8GemmArgs& a, const v4f (&acc)[MT][4], int64_t m0, int row0, int rows,
+                                             int64_t n0, int c0, int e)
+{
+    const bool cut = a.N - n0 < 256 && a.N % (ODT == F32 ? 4 : 8);
+    if (a.bias) {
+        if (cut) fp8_put<ODT, MT, true, true>(a, acc, m0, row0, rows, n0, c0, e);
+        else fp8_put<ODT, MT, true, false>(a, acc, m0, row0, rows, n0, c0, e);
+    } else {
+        if (cut) fp8_put<ODT, MT, false, true>(a, acc, m0, row0, rows, n0, c0, e);
+        else fp8_put<ODT, MT, false, false>(a, acc, m0, row0, rows, n0, c0, e);
+    }
+}
+
+// The gated epilogue of a wave: rows row0 + 16 mt of the tile, results 8 q .. + 7 of
+// the wave's 32 in this lane, gates in accumulators 0 and 1, ups in 2 and 3.  Four
+// waves make a block of 128 results, whose largest magnitude they find in LDS (top:
+// [wm][wn][row]); the stores are range-checked.
+template <int BM, bool BIAS>
+__device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[BM / 32][4], int64_t m0, int rows, int tn,
+                                              int wm, int wn, int j, int q, int e, uint32_t (*top)[4][BM / 2])
+{
+    constexpr int MT = BM / 32;
+    const int64_t F = a.N >> 1;
+    const int row0 = wm * (BM / 2) + j;
+    const int64_t f = (int64_t)tn * kFp8Block + wn * 32 + 8 * q;   // the lane's first result
+    const __amdgpu_buffer_rsrc_t rc = mx_rsrc(mx_uniform(a.out_codes + m0 * F), (int64_t)rows * F);
+    const __amdgpu_buffer_rsrc_t rs = mx_rsrc(mx_uniform((const uint8_t*)(a.out_scales + (int64_t)tn * a.R + m0)), rows * 4);
+    float bg[1][16], bu[1][16];
+    if constexpr (BIAS) {
+        mx_bias<1>(a, e, 0, F, f, bg);
+        mx_bias<1>(a, e, F, F, f, bu);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float g = acc[mt][i >> 2][i & 3], u = acc[mt][2 + (i >> 2)][i & 3];
+            if constexpr (BIAS) {
+                g = add_rn(g, bg[0][i]);
+                u = add_rn(u, bu[0][i]);
+            }
+            const float v = mx_gated(g, u);
+            acc[mt][i >> 2][i & 3] = v;
+            m = max(m, __float_as_uint(v) & 0x7fffffffu);
+        }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        if (q == 0) top[wm][wn][16 * mt + j] = m;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        uint32_t m = top[wm][0][16 * mt + j];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) m = max(m, top[wm][w][16 * mt + j]);
+        const Fp8Block b = fp8_block(m);
+        v2u c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c[i] = fp8_codes4(b, acc[mt][i][0], acc[mt][i][1], acc[mt][i][2], acc[mt][i][3]);
+        const uint32_t row = (uint32_t)(row0 + 16 * mt);
+        __builtin_amdgcn_raw_buffer_store_b64(c, rc, (int)(row * (uint32_t)F + (uint32_t)f), 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(b.scale), rs, wn == 0 && q == 0 ? (int)(row * 4) : (int)kOut, 0, 0);
+    }
+}
+
+// BM x 256 outputs per workgroup of eight waves (2 x 4, each BM/2 x 64, two to a
+// SIMD: with one wave the matrix core would wait for the fmas that read its results),
+// K in steps of 128, a scale block; one workgroup per CU, which takes tiles in turn.
+//   * A step's codes (128 bytes a row) and scales go global -> LDS by DMA into one of
+//     two or three slots, as many steps ahead of their use and, at a tile's end, into
+//     the next tiles' steps.  16-byte chunk c of LDS row r sits at c ^ ((r >> 1) & 7):
+//     a ds_read_b128 serves sixteen lanes a cycle (lanes {0-3, 12-15} of one group of
+//     sixteen and {4-11} of its neighbour), and these then hit sixteen different
+//     16-byte bank groups.
+//   * A wave holds all its weight fragments of a step (four column tiles) and walks
+//     the row tiles, whose fragments are read one tile ahead.  Before the last row
+//     tile the waves wait for the next step's DMA and meet: then nobody reads this
+//     step's slot any more, and the DMA furthest ahead goes out into it.  The next
+//     step's weight fragments replace this one's as the last MFMAs let go of them.
+//   * An MFMA's result joins the accumulators three MFMAs later.
+//   * LDS row 16 nt + i of a wave's 64 columns is column 16 (i >> 2) + 4 nt + (i & 3),
+//     so a lane ends with sixteen consecutive columns of one row.  Gated: a wave has
+//     32 gates (nt = 0, 1) and the 32 ups that belong to them, eight consecutive of
+//     each in a lane.
+template <int BM, bool GROUPED, bool GATED, bool HALF>
+__global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int tiles_m, int tiles_n)
+{
+    constexpr int MT = BM / 32, NT = 4, G = GATED ? 2 : 1;
+    // a slot: codes of both operands, scales of the rows, of the two weight blocks,
+    // and room for the scale DMA of waves that have none, so that all issue the same
+    constexpr int AB = BM * 128, BB = 256 * 128, SA = BM * 4, SLOT = AB + BB + SA + 512;
+    constexpr int SLOTS = BM == 256 ? 2 : 3;  // what LDS holds
+    constexpr int AI = BM / 64;               // A DMA instructions per wave (8 rows each)
+    constexpr int DMAS = AI + 4 + 1;          // all of a step's, per wave
+    constexpr int D1 = AI + 1;                // of them with the last row tile; the others follow
+    constexpr int PUTS = 2 * MT;              // stores of an epilogue, at least
+    __shared__ __align__(16) uint8_t smem[SLOTS * SLOT];
+    __shared__ uint32_t top[GATED ? 2 : 1][4][GATED ? BM / 2 : 1];
+
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int j = lane & 15, q = lane >> 4;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int64_t K = a.K, N = a.N;
+    const int nsteps = (int)fp8_blocks(K);
+    const int chunks = (int)(K >> 4);
+    const int64_t F = N >> 1;   // gated: number of results
+
+    // ---- tiles: this workgroup takes number blockIdx.x, + gridDim.x, ...
+    struct Tile {
+        int m0, rows, tn, e;   // rows 0: none
+    };
+    int ntiles;
+    if constexpr (GROUPED) {
+        MxRows r;
+        ntiles = (int)mx_find<BM, false>(a, 0, r) * tiles_n;
+        fp8_zero_rows(a, blockIdx.x, gridDim.x);
+    } else {
+        ntiles = tiles_m * tiles_n;
+    }
+    // Lane i of every wave holds the workgroup's i-th tile of a batch of 64.
+    Tile mine;
+    auto fill = [&](int batch) {
+        mine = Tile{0, 0, 0, 0};
+        const int64_t at = blockIdx.x + (int64_t)(batch * 64 + lane) * gridDim.x;
+        const bool have = at < ntiles;
+        // each XCD (workgroup index modulo 8; the grid is a multiple of 8 or
+        // the tiles are its first) takes a contiguous range
+        const int t = have ? (int)at : 0, q8 = ntiles >> 3, r8 = ntiles & 7, xcd = t & 7;
+        const int tile = xcd * q8 + min(xcd, r8) + (t >> 3);
+        if constexpr (GROUPED) {
+            mx_rows_of<BM>(a, tile, tiles_n, mine.e, mine.m0, mine.tn, mine.rows);
+            if (!have) mine.rows = 0;
+        } else {
+            // groups of four row tiles: an XCD's 32 concurrent tiles span 4 x 8 blocks
+            const int per = 4 * tiles_n, grp = tile / per, gm = min(tiles_m - grp * 4, 4), in_g = tile - grp * per;
+            mine.m0 = (grp * 4 + in_g % gm) * BM;
+            mine.tn = in_g / gm;
+            mine.rows = have ? (int)min(a.M - mine.m0, (int64_t)BM) : 0;
+        }
+    };
+    auto tile_of = [&](int i) {
+        if (i && !(i & 63)) fill(i >> 6);
+        const int l = i & 63;
+        return Tile{__builtin_amdgcn_readlane(mine.m0, l), __builtin_amdgcn_readlane(mine.rows, l),
+                    __builtin_amdgcn_readlane(mine.tn, l), __builtin_amdgcn_readlane(mine.e, l)};
+    };
+
+    // ---- DMA: wave w moves rows [w BM/8, (w + 1) BM/8) of A and 32 weight columns
+    const int l8 = lane >> 3, ar0 = wave * (BM / 8);
+    const int ch = (lane & 7) ^ (lane >> 4);   // chunk of this lane; bit 2 of the LDS row's half turns it into ch ^ 4
+    const bool gather = GROUPED && a.rows != nullptr;
+    // Every resource is 2^31 bytes long: a lane that has nothing to read (a row
+    // or column past the tile's, no tile, a chunk past K) has an offset past
+    // that and gets zeros.
+    uint32_t avo[AI], bvo[4], svo;   // lane offsets of codes and scales
+    int sstep = 0;                   // bytes from a step's scales to the next's
+    __amdgpu_buffer_rsrc_t ra, rb, rs;
+    auto a_half = [&](int i) { return BM == 64 ? wave & 1 : i & 1; };   // whether A's instruction i takes ch ^ 4
+    auto set_dma = [&](const Tile& t) {
+        // the source row of tile row i, or none
+        auto src_row = [&](int i) -> int64_t {
+            if (i >= t.rows) return -1;
+            if (!gather) return i;
+            const int64_t s = a.rows[(int64_t)t.m0 + i];
+            return s >= 0 && s < a.M ? s : -1;
+        };
+#pragma unroll
+        for (int i = 0; i < AI; ++i) {
+            const int64_t s = src_row(ar0 + 8 * i + l8);
+            avo[i] = s < 0 ? kOut : (uint32_t)(s * K + (ch ^ (a_half(i) * 4)) * 16);
+        }
+        ra = mx_rsrc(mx_uniform(gather ? a.a : a.a + (int64_t)t.m0 * K), kOut);
+        // LDS rows 32 wave + 8 i + l8: column tile nt, row idx of it
+        const int64_t ncols = t.rows == 0 ? 0 : GATED ? F : N;
+        const int64_t col0 = (int64_t)t.tn * (GATED ? 128 : 256);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int nt = (wave & 1) * 2 + (i >> 1), idx = (i & 1) * 8 + l8;
+            const int c = GATED ? wn * 32 + 8 * (idx >> 2) + 4 * (nt & 1) + (idx & 3)
+                                : wn * 64 + 16 * (idx >> 2) + 4 * nt + (idx & 3);
+            bvo[i] = col0 + c < ncols ? (uint32_t)(c * (uint32_t)K + (ch ^ ((i & 1) * 4)) * 16) : kOut;
+        }
+        const int64_t brow = (int64_t)t.e * N + col0 + (GATED && (wave & 1) ? F : 0);
+        rb = mx_rsrc(mx_uniform(a.b + (t.rows ? brow : 0) * K), kOut);
+        // scales: of 64 rows, or of the two weight blocks
+        if (wave < BM / 64) {
+            const int64_t s = src_row(wave * 64 + lane);
+            svo = s < 0 ? kOut : (uint32_t)(s * 4);
+            rs = mx_rsrc(mx_uniform((const uint8_t*)(gather ? a.sa : a.sa + t.m0)), kOut);
+            sstep = (int)(a.M * 4);
+        } else {
+            const int64_t blocks = fp8_blocks(N), nb = GATED ? t.tn : 2 * t.tn, up = GATED ? F / kFp8Block : 1;
+            const bool have = wave == BM / 64 && lane < 2 && t.rows != 0 && nb + lane * up < blocks;
+            svo = have ? (uint32_t)(lane * up * nsteps * 4) : kOut;
+            rs = mx_rsrc(mx_uniform((const uint8_t*)(a.sb + ((int64_t)t.e * blocks + (t.rows ? nb : 0)) * nsteps)), kOut);
+            sstep = 4;
+        }
+    };
+    // the scale DMA's place in a slot
+    const int sdst = AB + BB + (wave < BM / 64 ? wave * 256 : wave == BM / 64 ? SA : SA + 256);
+
+    // The DMA of one step, an instruction at a time: `Dma` holds what its
+    // instructions share.
+    struct Dma {
+        int ko, so;          // offsets of the step in a row of codes and in the scales
+        uint32_t t0, t1;     // kOut where the chunk, its partner lies past K
+    };
+    auto dma_of = [&](Dma& d, int s) {
+        d.t0 = s * 8 < chunks - ch ? 0u : kOut;
+        d.t1 = s * 8 < chunks - (ch ^ 4) ? 0u : kOut;
+        d.ko = s * 128;
+        d.so = s * sstep;
+    };
+    auto dma = [&](const Dma& d, int sl, int n) {
+        if (n < AI) {
+            mx_dma<16>(ra, smem + sl + (ar0 + 8 * n) * 128, avo[n < AI ? n : 0] | (a_half(n) ? d.t1 : d.t0), d.ko);
+        } else if (n == AI) {
+            mx_dma<4>(rs, smem + sl + sdst, svo, d.so);
+        } else {
+            const int i = n - AI - 1;
+            mx_dma<16>(rb, smem + sl + AB + (wave * 32 + 8 * i) * 128, bvo[i & 3] | ((i & 1) ? d.t1 : d.t0), d.ko);
+        }
+    };
+    // The steps of all tiles form one sequence; the DMA runs SLOTS steps, so up
+    // to as many tiles, ahead of the MFMAs.
+    fill(0);
+    Tile cur = tile_of(0), q0{0, 0, 0, 0}, q1 = q0, q2 = q0;
+    if (cur.rows == 0) return;
+    int t_dma = 0, s_dma = 0, ahead = 0;
+    set_dma(cur);
+    auto advance = [&]() {
+        if (++s_dma < nsteps) return;
+        s_dma = 0;
+        const Tile t = tile_of(++t_dma);
+        set_dma(t);
+        // (by value: a choice of addresses would put the queue in memory)
+        auto put = [&](Tile& x, bool here) {
+            x.m0 = here ? t.m0 : x.m0;
+            x.rows = here ? t.rows : x.rows;
+            x.tn = here ? t.tn : x.tn;
+            x.e = here ? t.e : x.e;
+        };
+        put(q0, ahead == 0);
+        put(q1, ahead == 1);
+        if constexpr (SLOTS == 3) put(q2, ahead == 2);
+        ++ahead;
+    };
+
+    // ---- fragments: LDS rows ao + 16 mt and bo + 16 nt, chunks q and q + 4
+    const int sw = (q ^ ((j >> 1) & 7)) * 16;
+    const int ao = (wm * (BM / 2) + j) * 128 + sw, bo = AB + (wn * 64 + j) * 128 + sw;
+    const int sao = AB + BB + (wm * (BM / 2) + j) * 4, sbo = AB + BB + SA + (GATED ? 0 : (wn >> 1) * 4);
+    v8i fa[2], fb[NT];
+    float sa[2], sb[G];
+    // (base: a lane's address in a slot, off: the row tile's, which is an immediate)
+    auto read = [&](v8i& f, int base, int off) {
+        const v4i lo = *(const v4i*)(smem + base + off), hi = *(const v4i*)(smem + (base ^ 64) + off);
+        f = join(lo, hi);
+    };
+    // row tile mt of a slot: its fragment and scales
+    auto read_a = [&](int sl, int mt) {
+        read(fa[mt & 1], sl + ao, mt * 16 * 128);
+        sa[mt & 1] = *(const float*)(smem + sl + sao + mt * 64);
+    };
+    auto read_sb = [&](int sl) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) sb[i] = *(const float*)(smem + sl + sbo + 4 * i);
+    };
+
+    Dma d;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+        dma_of(d, s_dma);
+#pragma unroll
+        for (int n = 0; n < DMAS; ++n) dma(d, s * SLOT, n);
+        if (s + 1 < SLOTS) advance();
+    }
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((SLOTS - 1) * DMAS) : "memory");   // the first step has landed
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int n = 0; n < NT; ++n) read(fb[n], bo, n * 16 * 128);
+    read_a(0, 0);
+    read_sb(0);
+    int sl = 0, stores = 0;                // stores: steps in which the last epilogue's may be in flight
+    for (;;) {
+        v4f acc[MT][NT], tmp[4];
+        float f[2][G];                     // factors of a row tile, and of the one before
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[mt][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmp[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < G; ++g) f[1][g] = 0.0f;
+        // result i of a step joins its accumulators
+        auto join_in = [&](int i) {
+            v4f& c = acc[i >> 2][i & 3];
+            const float x = f[(i >> 2) & 1][GATED ? (i & 3) >> 1 : 0];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(tmp[i & 3][r], x, c[r]);
+            asm volatile("" : "+v"(c));   // here, not behind the next branch
+        };
+        int behind = 0;   // the step before has DMA left to send
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < nsteps; ++s) {
+            const int nx = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
+            asm volatile("" : "+s"(behind));
+            v8h hb[HALF ? NT : 1][4], ha[4];
+            if constexpr (HALF) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) fp8_to_f16(fb[n], hb[n]);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (m == MT - 1) {
+                    // The next step has landed, and this one is read.  Still in flight
+                    // may be the DMA of the steps after the next and, in a tile's first
+                    // SLOTS - 1 steps, the stores of the tile before, which went out
+                    // after it.
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\t"
+                                 "s_cmp_lt_i32 %0, 1\n\t"
+                                 "s_cbranch_scc1 1f\n\t"
+                                 "s_waitcnt vmcnt(%1)\n\t"
+                                 "s_branch 2f\n"
+                                 "1:\n\t"
+                                 "s_waitcnt vmcnt(%2)\n"
+                                 "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"((SLOTS - 2) * DMAS + PUTS),
+                                 "n"((SLOTS - 2) * DMAS)
+                                 : "memory", "scc");
+                    --stores;
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if constexpr (HALF) fp8_to_f16(fa[m & 1], ha);
+#pragma unroll
+                for (int g = 0; g < G; ++g) f[m & 1][g] = mul_rn(sa[m & 1], sb[g]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int i = m * NT + n;
+                    if constexpr (HALF) tmp[i & 3] = f16_mfma(hb[n], ha);
+                    else tmp[i & 3] = fp8_mfma(fb[n], fa[m & 1]);
+                    if (m < MT - 1) {
+                        if (n == 0) read_a(sl, m + 1);
+                    } else {
+                        // (past the last step: of a slot's older contents, unused)
+                        if (n == 0) read_a(nx, 0);
+                        read(fb[n], nx + bo, n * 16 * 128);
+                        if (n == NT - 1) read_sb(nx);
+#pragma unroll
+                        for (int x = n * D1 / NT; x < (n + 1) * D1 / NT; ++x) dma(d, sl, x);
+                    }
+                    join_in(i >= 3 ? i - 3 : MT * NT - 3 + i);
+                    if (m == 0) {
+                        // the rest of the DMA that the step before began (a tile's
+                        // first step: it went out before the epilogue)
+                        if (n == 0 && behind) {
+                            const int pv = sl == 0 ? (SLOTS - 1) * SLOT : sl - SLOT;
+#pragma unroll
+                            for (int x = D1; x < DMAS; ++x) dma(d, pv, x);
+                        }
+                        if (n == 2) {
+                            advance();
+                            dma_of(d, s_dma);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            behind = 1;
+            sl = nx;
+        }
+        const int pv = sl == 0 ? (SLOTS - 1) * SLOT : sl - SLOT;
+#pragma unroll
+        for (int x = D1; x < DMAS; ++x) dma(d, pv, x);
+#pragma unroll
+        for (int i = MT * NT - 3; i < MT * NT; ++i) join_in(i);
+
+        // ---- epilogue
+        const int row0 = wm * (BM / 2) + j;
+        if constexpr (GATED) {
+            if (a.bias) fp8_put_gated<BM, true>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, top);
+            else fp8_put_gated<BM, false>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, top);
+        } else {
+            const int64_t n0 = (int64_t)cur.tn * 256;
+            const int c0 = wn * 64 + 16 * q;
+            if constexpr (HALF) fp8_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+            else if (a.out_dtype == BF16) fp8_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+            else fp8_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+        }
+        stores = SLOTS - 1;
+        cur = q0;
+        q0 = q1;
+        if constexpr (SLOTS == 3) q1 = q2;
+        --ahead;
+        if (cur.rows == 0) break;
+    }
+}
+
+int skinny_rows(const Fp8GemmArgs& a)
+{
+    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+template <int MT, int NT, int KW, bool GATED, bool HALF = false> hipError_t launch_skinny_w(const Fp8GemmArgs& a, hipStream_t st)
+{
+    constexpr int COLS = (GATED ? 16 : 16 * NT) * (kSkinnyWaves / KW);
+    const int64_t n = GATED ? a.N / 2 : a.N;
+    const unsigned tn = (unsigned)((n + COLS - 1) / COLS);
+    if (a.E) {
+        const unsigned tm = (unsigned)(a.R / (16 * MT) + (a.E < a.R ? a.E : a.R) + 1);
+        hipLaunchKernelGGL((fp8_skinny_kernel<MT, NT, KW, true, GATED, HALF>), dim3(tn, tm), dim3(512), 0, st, a);
+    } else if constexpr (!GATED) {
+        hipLaunchKernelGGL((fp8_skinny_kernel<MT, NT, KW, false, false, HALF>), dim3(tn, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
+                           dim3(512), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
+template <int MT> hipError_t launch_skinny(const Fp8GemmArgs& a, hipStream_t st)
+{
+    if (a.out_codes) return launch_skinny_w<MT, 2, 1, true>(a, st);
+    if (a.out_dtype == F32) return launch_skinny_w<MT, 1, 8, false, true>(a, st);
+    return launch_skinny_w<MT, 1, 8, false>(a, st);
+}
+
+// One workgroup per CU (LDS holds one), which takes tiles in turn.
+constexpr int64_t kTileGrid = 256;
+
+template <int BM, bool HALF> hipError_t launch_tile(const Fp8GemmArgs& a, hipStream_t st)
+{
+    const bool gated = a.out_codes != nullptr;
+    const int64_t tn = gated ? a.N / 2 / kFp8Block : (a.N + 255) / 256;
+    // (grouped: at most this many, the device knows)
+    const int64_t tm = a.E ? a.R / BM + (a.E < a.R ? a.E : a.R) : (a.M + BM - 1) / BM;
+    const unsigned grid = (unsigned)(tm * tn < kTileGrid ? tm * tn : kTileGrid);
+    if (!a.E)
+        hipLaunchKernelGGL((fp8_tile_kernel<BM, false, false, HALF>), dim3(grid), dim3(512), 0, st, a, (int)tm, (int)tn);
+    else if (!gated)
+        hipLaunchKernelGGL((fp8_tile_kernel<BM, true, false, HALF>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
+    else if constexpr (!HALF)
+        hipLaunchKernelGGL((fp8_tile_kernel<BM, true, true, false>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int fp8_gemm_path(const Fp8GemmArgs& a)
+{
+    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
+    const bool half = !a.out_codes && a.out_dtype == F32;
+    // A tile's outputs are addressed with 31 bits: rows of 8 MB and more are the
+    // skinny kernel's.
+    if (a.N * (a.out_codes ? 1 : a.out_dtype == F32 ? 4 : 2) >= (int64_t)1 << 23) return kFp8Skinny;
+    if (rows <= 64) return kFp8Skinny;
+    if (half) return kFp8Tile128;
+    return rows <= 128 ? kFp8Tile64 : rows <= 512 ? kFp8Tile128 : kFp8Tile256;
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t st)
+{
+    const bool half = !a.out_codes && a.out_dtype == F32;
+    switch (fp8_gemm_path(a)) {
+    case kFp8Tile256: return launch_tile<256, false>(a, st);
+    case kFp8Tile128: return half ? launch_tile<128, true>(a, st) : launch_tile<128, false>(a, st);
+    case kFp8Tile64: return launch_tile<64, false>(a, st);
+    }
+    const int rows = skinny_rows(a);
+    return rows == 16 ? launch_skinny<1>(a, st) : rows == 32 ? launch_skinny<2>(a, st) : launch_skinny<4>(a, st);
+}
+
+}  // namespace w4a4

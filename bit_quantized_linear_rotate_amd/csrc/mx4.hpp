@@ -82,6 +82,20 @@ struct RouteArgs {
 int64_t route_chunks(int64_t T);   // 1: no workspace needed
 hipError_t launch_route(const RouteArgs& a, hipStream_t st);
 
+// Routing by scores: an expert's score is the softmax over all experts or the sigmoid
+// of its logit, its choice value the score plus a bias; the best top_groups of
+// `groups` equal groups of neighbouring experts stay (a group's worth: its largest
+// choice value, or the sum of its two largest), then the best k experts in them.
+// Weights: scores, over their sum if renormalize, times scale.
+constexpr int kRouteMaxGroups = 64;
+struct RouteScoredArgs : RouteArgs {
+    int sigmoid;                   // scores: sigmoid (1) or softmax (0)
+    const float* bias;             // (E,) or nullptr
+    int groups, top_groups, group_best;
+    float scale;
+};
+hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t st);
+
 // out[t] = sum_j weights[t][j] * y[pos[t][j]], fp32, j in order
 struct CombineArgs {
     const void* y;                 // (R, N)

@@ -161,8 +161,25 @@ __device__ __forceinline__ void scan_experts(const int* tot, int* off, int E)
     }
 }
 
-// top-k of a chunk's tokens and the chunk's slots per expert.  ONE: the only
-// chunk, which then sorts its own slots.
+// The end of a chunk whose slots per expert are counted.  ONE: the only chunk,
+// which then sorts its own slots.
+template <bool ONE> __device__ __forceinline__ void route_chunk_done(const RouteArgs& a, int* cnt, int* off)
+{
+    const int tid = threadIdx.x;
+    if constexpr (ONE) {
+        scan_experts(cnt, off, a.E);
+        __syncthreads();
+        const int total = off[a.E];
+        for (int e = tid; e <= a.E; e += 1024) a.offsets[e] = off[e];
+        for (int64_t i = total + tid; i < a.T * a.k; i += 1024) a.rows[i] = -1;
+        __syncthreads();
+        place_slots(a, 0, a.T * a.k, off);
+    } else {
+        for (int e = tid; e < a.E; e += 1024) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+    }
+}
+
+// top-k of a chunk's tokens and the chunk's slots per expert.
 template <int DT, int L, int NV, bool ONE> __global__ __launch_bounds__(1024) void route_kernel(RouteArgs a, int64_t chunk)
 {
     __shared__ int cnt[kRouteMaxExperts], off[kRouteMaxExperts + 1];
@@ -183,17 +200,192 @@ template <int DT, int L, int NV, bool ONE> __global__ __launch_bounds__(1024) vo
         }
     }
     __syncthreads();
-    if constexpr (ONE) {
-        scan_experts(cnt, off, a.E);
-        __syncthreads();
-        const int total = off[a.E];
-        for (int e = tid; e <= a.E; e += 1024) a.offsets[e] = off[e];
-        for (int64_t i = total + tid; i < a.T * a.k; i += 1024) a.rows[i] = -1;
-        __syncthreads();
-        place_slots(a, 0, a.T * a.k, off);
-    } else {
-        for (int e = tid; e < a.E; e += 1024) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+    route_chunk_done<ONE>(a, cnt, off);
+}
+
+// ---- routing by scores -------------------------------------------------------
+// The choice is made in double precision: in fp32 the rounding of a score would
+// decide between experts whose choice values differ by a few parts in 2^24, which a
+// batch of some thousand tokens holds.  Without a bias the scores' order is the
+// logits'.
+
+// the value of the lane whose index differs in bits D, for the lanes of one token
+template <int L> __device__ __forceinline__ double lanes_max64(double v)
+{
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) v = fmax(v, __shfl_xor(v, d));
+    return v;
+}
+template <int L> __device__ __forceinline__ double lanes_sum64(double v)
+{
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+// The lane (of the wave) with the token's largest v, the lowest of several; -1 where
+// every v is -inf
+template <int L> __device__ __forceinline__ int first_best(double v, double& best)
+{
+    best = lanes_max64<L>(v);
+    const unsigned long long hit = __ballot(v == best && best > -__builtin_inf());
+    const int base = L == 64 ? 0 : (threadIdx.x & 63) & ~(L - 1);
+    const unsigned long long mine = L == 64 ? hit : (hit >> base) & ((1ull << (L & 63)) - 1);
+    return mine ? base + __builtin_ctzll(mine) : -1;
+}
+
+// One token by L lanes, NV consecutive experts each: choice r ends in lane r.  worth:
+// this token's E choice values in LDS (GROUPS only).
+template <int L, int NV, bool GROUPS>
+__device__ __forceinline__ void route_scored_token(const RouteScoredArgs& a, int64_t t, bool live, int lane, double* worth,
+                                                   int& expert, float& weight)
+{
+    const double none = -__builtin_inf();
+    const int e0 = lane * NV;
+    double score[NV], val[NV];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = e0 + i;
+        // (+ 0: both zeros are the same logit; a NaN is no logit)
+        const float l = live && e < a.E ? add_rn(load_any_f32(a.dtype, a.logits, t * a.stride + e), 0.0f) : -__builtin_inff();
+        val[i] = l > -__builtin_inff() ? (double)l : none;
+        top = fmaxf(top, (float)val[i]);
     }
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) score[i] = val[i] > none ? 1.0 / (1.0 + exp(-val[i])) : 0.0;
+    } else {
+        const double m = lanes_max64<L>((double)top);
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            // (equal to the largest, which may be infinite: 1)
+            score[i] = val[i] > none ? (val[i] == m ? 1.0 : exp(val[i] - m)) : 0.0;
+            sum += score[i];
+        }
+        sum = lanes_sum64<L>(sum);
+        const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) score[i] *= inv;
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const double v = score[i] + (double)(e0 + i < a.E ? a.bias[e0 + i] : 0.0f);
+            val[i] = val[i] > none && v > none ? v : none;
+        }
+    }
+    if constexpr (GROUPS) {
+        const int size = a.E / a.groups;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e0 + i < a.E) worth[e0 + i] = val[i] > none ? (a.bias ? val[i] : score[i]) : none;
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+        constexpr int GN = kRouteMaxGroups / L;   // groups of a lane, neighbours
+        const int gn = (a.groups + L - 1) / L;
+        double of[GN];
+#pragma unroll
+        for (int i = 0; i < GN; ++i) {
+            const int g = lane * gn + i;
+            of[i] = none;
+            if (i < gn && g < a.groups) {
+                double m1 = none, m2 = none;
+                for (int x = 0; x < size; ++x) {
+                    const double v = worth[g * size + x];
+                    m2 = fmax(m2, fmin(m1, v));
+                    m1 = fmax(m1, v);
+                }
+                of[i] = a.group_best == 2 && m2 > none ? m1 + m2 : m1;
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        unsigned long long kept = 0;
+        for (int r = 0; r < a.top_groups; ++r) {
+            double mine = of[0], best;
+#pragma unroll
+            for (int i = 1; i < GN; ++i) mine = fmax(mine, of[i]);
+            const int from = first_best<L>(mine, best);
+            int g = 0;
+#pragma unroll
+            for (int i = GN - 1; i >= 0; --i)
+                if (of[i] == best) g = i;
+            if (lane == (from & (L - 1)) && from >= 0) {
+#pragma unroll
+                for (int i = 0; i < GN; ++i)
+                    if (i == g) of[i] = none;
+            }
+            g = __shfl(lane * gn + g, from < 0 ? 0 : from);
+            if (from >= 0) kept |= 1ull << g;
+        }
+        int g = e0 / size, left = (g + 1) * size - e0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (left == 0) {
+                ++g;
+                left = size;
+            }
+            --left;
+            if (!((kept >> (g & 63)) & 1)) val[i] = none;
+        }
+    }
+    expert = -1;
+    double mine = 0.0;
+    for (int r = 0; r < a.k; ++r) {
+        double m = val[0], best;
+#pragma unroll
+        for (int i = 1; i < NV; ++i) m = fmax(m, val[i]);
+        const int from = first_best<L>(m, best);
+        int at = 0;
+        double s = score[0];
+#pragma unroll
+        for (int i = NV - 1; i >= 0; --i)
+            if (val[i] == best) {
+                at = i;
+                s = score[i];
+            }
+        const bool won = from >= 0 && lane == (from & (L - 1));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (won && i == at) val[i] = none;
+        const int src = from < 0 ? 0 : from, e = __shfl(e0 + at, src);
+        s = __shfl(s, src);
+        if (from >= 0 && lane == r) {
+            expert = e;
+            mine = s;
+        }
+    }
+    if (a.renormalize) {
+        const double sum = lanes_sum64<L>(mine);
+        mine = sum > 0.0 ? mine / sum : 0.0;
+    }
+    weight = (float)(mine * (double)a.scale);
+}
+
+template <int L, int NV, bool GROUPS, bool ONE>
+__global__ __launch_bounds__(1024) void route_scored_kernel(RouteScoredArgs a, int64_t chunk)
+{
+    __shared__ int cnt[kRouteMaxExperts], off[kRouteMaxExperts + 1];
+    __shared__ double worth[GROUPS ? 1024 / L : 1][GROUPS ? L * NV : 1];
+    const int tid = threadIdx.x, lane = tid & (L - 1);
+    for (int e = tid; e < a.E; e += 1024) cnt[e] = 0;
+    __syncthreads();
+    const int64_t t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, a.T);
+    // (all lanes of a wave stay in the loop: lanes read one another)
+    for (int64_t tw = t0 + (tid >> 6) * (64 / L); tw < t1; tw += 1024 / L) {
+        const int64_t t = tw + ((tid & 63) / L);
+        int e;
+        float w;
+        route_scored_token<L, NV, GROUPS>(a, t, t < t1, lane, worth[GROUPS ? tid / L : 0], e, w);
+        if (lane < a.k && t < t1) {
+            a.weights[t * a.k + lane] = w;
+            a.experts[t * a.k + lane] = e;
+            if (e >= 0) atomicAdd(&cnt[e], 1);
+        }
+    }
+    __syncthreads();
+    route_chunk_done<ONE>(a, cnt, off);
 }
 
 constexpr int kSortThreads = 512;
@@ -232,18 +424,27 @@ __global__ __launch_bounds__(kSortThreads) void route_sort_kernel(RouteArgs a, i
     place_slots(a, t0 * a.k, t1 * a.k, off);
 }
 
-template <int DT, int L, int NV> hipError_t route_nv(const RouteArgs& a, hipStream_t st)
+// `kernel` on the chunks of a.T tokens, then, where there is more than one, the sort
+template <class Args> hipError_t route_launch(const Args& a, void (*one)(Args, int64_t), void (*many)(Args, int64_t), hipStream_t st)
 {
     const int64_t chunks = route_chunks(a.T), chunk = (a.T + chunks - 1) / chunks;
-    if (chunks == 1) {
-        hipLaunchKernelGGL((route_kernel<DT, L, NV, true>), dim3(1), dim3(1024), 0, st, a, chunk);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((route_kernel<DT, L, NV, false>), dim3((unsigned)chunks), dim3(1024), 0, st, a, chunk);
+    hipLaunchKernelGGL(chunks == 1 ? one : many, dim3((unsigned)chunks), dim3(1024), 0, st, a, chunk);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || chunks == 1) return e;
     hipLaunchKernelGGL(route_sort_kernel, dim3((unsigned)chunks), dim3(kSortThreads), 0, st, a, chunk, (int)chunks);
     return hipGetLastError();
+}
+
+template <int DT, int L, int NV> hipError_t route_nv(const RouteArgs& a, hipStream_t st)
+{
+    return route_launch<RouteArgs>(a, route_kernel<DT, L, NV, true>, route_kernel<DT, L, NV, false>, st);
+}
+
+template <int L, int NV> hipError_t route_scored_nv(const RouteScoredArgs& a, hipStream_t st)
+{
+    if (a.groups > a.top_groups)
+        return route_launch<RouteScoredArgs>(a, route_scored_kernel<L, NV, true, true>, route_scored_kernel<L, NV, true, false>, st);
+    return route_launch<RouteScoredArgs>(a, route_scored_kernel<L, NV, false, true>, route_scored_kernel<L, NV, false, false>, st);
 }
 
 template <int DT> hipError_t route_dt(const RouteArgs& a, hipStream_t st)
@@ -341,6 +542,14 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st)
     case BF16: return route_dt<BF16>(a, st);
     }
     return hipErrorNotSupported;
+}
+
+hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t st)
+{
+    if (a.E <= 256 && a.k <= 16)
+        return a.E <= 32 ? route_scored_nv<16, 2>(a, st) : a.E <= 64 ? route_scored_nv<16, 4>(a, st)
+               : a.E <= 128 ? route_scored_nv<16, 8>(a, st) : route_scored_nv<16, 16>(a, st);
+    return a.E <= 256 ? route_scored_nv<64, 4>(a, st) : route_scored_nv<64, 16>(a, st);
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st)

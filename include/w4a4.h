@@ -442,6 +442,104 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
                           size_t workspace_bytes, void* stream);
 
 /*
+ * Block-scaled 8-bit floating point (fp8), dense and grouped by expert, and routing
+ * by scores.
+ *   Format.  Codes are OCP e4m3 bytes (bias 7, largest 448, no infinities, 0x7f and
+ *   0xff NaN), (rows, K), 16-byte aligned, under fp32 scales.  Activations: one scale
+ *   per row and 128 consecutive k, k-block-major: block b of row r at b * rows + r.
+ *   Weights (N, K): one per 128 rows by 128 k, (ceil(N/128), ceil(K/128)) row-major.
+ *   Blocks at the ends may be short.  Quantising: A = max(absmax, 448 * 2^-126) of
+ *   the block, scale = A / 448, code = e4m3(448 y / A) to nearest, ties to the even
+ *   code (the product and the quotient each in fp32); a block that holds a NaN or an
+ *   infinity gets the scale NaN and codes 0.  K is a multiple of 16, at most 2^22; at
+ *   most 2^28 rows.  The products refuse (W4A4_UNSUPPORTED) activations of more than
+ *   2^31 bytes of scales, codes of more than 2^31 bytes behind a row index (so the
+ *   expert layer's x), more than 16384 experts, and outputs of R x N (M x N) with
+ *   (R / 64 + E + 1) (N / 128 + 1) >= 2^22.
+ *
+ * w8a8_quantize_fp8: rows of x (any strides; 16-byte aligned contiguous rows take
+ *   wide loads), rotated first if g > 0, as for w4a4_quantize_mx4.
+ * w8a8_quantize_weights_fp8: E matrices of weights (N, K), `stride_e` elements apart,
+ *   each in blocks of its own, rotated along k first if g > 0; codes (E, N, K),
+ *   scales (E, ceil(N/128), ceil(K/128)); E <= 65535.
+ * w8a8_dequantize_fp8, w8a8_dequantize_weights_fp8: the values in out_dtype (code
+ *   times scale in fp32, rounded once more to 16 bits), 16-byte aligned.
+ * w8a8_gemm_fp8: out[m][n] = O(sum_b sa[b][m] sw[n/128][b] (sum_{k in b} a[m][k]
+ *   w[n][k]) + bias[n]), fp32 sums, the inner ones on the matrix cores.
+ * w8a8_linear_fp8: quantiser and product back to back; bias in x_dtype; a workspace
+ *   of w8a8_linear_fp8_workspace_size(M, K) bytes, 16-byte aligned.
+ * w8a8_grouped_gemm_fp8: sorted rows, offsets and row index as for
+ *   w4a4_grouped_gemm_mx4; weights (E, N, K), scales (E, ceil(N/128), ceil(K/128)),
+ *   bias (E, N).  Rows before offsets[0] and from offsets[E] on become zeros.
+ * w8a8_grouped_gated_fp8: the same product with N/2 gates followed by N/2 ups (N a
+ *   multiple of 256); the result is the fp8 form of silu(gate) * up, taken from the
+ *   fp32 sums: out_codes (R, N/2), out_scales (N/256, R).
+ * w8a8_gemm_fp8_plan (host-only): the kernel these calls take for `rows` rows (E = 0:
+ *   dense; 16-bit outputs): 0 skinny, 1 / 2 / 3 tiles of 64 / 128 / 256 rows, -1 none.
+ * w4a4_route_experts_scored: an expert's score is the softmax over all E (sigmoid =
+ *   0) or the sigmoid of its logit, its choice value the score plus bias[e] (fp32,
+ *   NULL: none).  With groups > top_groups, the experts are `groups` equal runs of
+ *   neighbours, and the top_groups of largest worth stay: a group's worth is its
+ *   largest choice value (group_best = 1) or the sum of its two largest (2; of one,
+ *   where only one can be taken).  Of those the top_k experts by choice value (without
+ *   a bias: by logit); ties of groups and experts go to the lower index.  Scores and
+ *   choice are in double precision.  weights: the chosen experts' scores (without the
+ *   bias), over their sum (renormalize != 0; a sum of zero gives zeros), times scale.
+ *   NaN and -inf logits and choice values are never taken; experts whose logits are
+ *   +inf share a softmax.  Outputs, workspace and limits as for w4a4_route_experts;
+ *   groups <= 64 divides E, top_k <= (E / groups) * top_groups.
+ * w8a8_experts_fp8: w4a4_route_experts_scored, quantise, gated product (w13: (E, 2 F,
+ *   K), gates first, F a multiple of 128), product (w2: (E, K, F)), combine; the
+ *   experts' rows are kept in rows_dtype, x_dtype (a 16-bit layer then rounds twice)
+ *   or W4A4_F32.  No biases of the products; T * top_k < 2^28.  Workspace of
+ *   w8a8_experts_fp8_workspace_size(.., rows_dtype) bytes, 16-byte aligned.
+ */
+int w8a8_quantize_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                      int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                      uint8_t* codes, float* scales, void* stream);
+int w8a8_quantize_weights_fp8(const void* w, int w_dtype, int64_t E, int64_t N, int64_t K,
+                              int64_t stride_e, int64_t stride_n, int64_t stride_k, int32_t g,
+                              const int8_t* sign_in, const int8_t* sign_out, uint8_t* codes,
+                              float* scales, void* stream);
+int w8a8_dequantize_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K, void* out,
+                        int out_dtype, void* stream);
+int w8a8_dequantize_weights_fp8(const uint8_t* codes, const float* scales, int64_t E, int64_t N,
+                                int64_t K, void* out, int out_dtype, void* stream);
+int w8a8_gemm_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
+                  const uint8_t* w_codes, const float* w_scales, int64_t N, const void* bias,
+                  int bias_dtype, void* out, int out_dtype, void* stream);
+int w8a8_gemm_fp8_plan(int64_t rows, int64_t K, int64_t N, int32_t E, int32_t gated, int* kernel);
+size_t w8a8_linear_fp8_workspace_size(int64_t M, int64_t K);
+int w8a8_linear_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                    int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                    const uint8_t* w_codes, const float* w_scales, int64_t N, const void* bias,
+                    void* out, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int w8a8_grouped_gemm_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
+                          const uint8_t* w_codes, const float* w_scales, int32_t E, int64_t N,
+                          const int32_t* offsets, const int32_t* rows, int64_t R, const void* bias,
+                          int bias_dtype, void* out, int out_dtype, void* stream);
+int w8a8_grouped_gated_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
+                           const uint8_t* w_codes, const float* w_scales, int32_t E, int64_t N,
+                           const int32_t* offsets, const int32_t* rows, int64_t R, const void* bias,
+                           int bias_dtype, uint8_t* out_codes, float* out_scales, void* stream);
+int w4a4_route_experts_scored(const void* logits, int dtype, int64_t T, int64_t stride, int32_t E,
+                              int32_t top_k, int32_t sigmoid, const float* bias, int32_t groups,
+                              int32_t top_groups, int32_t group_best, int32_t renormalize,
+                              float scale, float* weights, int32_t* experts, int32_t* rows,
+                              int32_t* pos, int32_t* offsets, void* workspace,
+                              size_t workspace_bytes, void* stream);
+size_t w8a8_experts_fp8_workspace_size(int64_t T, int64_t K, int64_t F, int32_t E, int32_t top_k,
+                                       int rows_dtype);
+int w8a8_experts_fp8(const void* x, int x_dtype, int64_t T, int64_t K, int64_t stride_m,
+                     int64_t stride_k, int32_t g, const int8_t* sign_in, const int8_t* sign_out,
+                     const void* logits, int logits_dtype, int64_t logits_stride, int32_t E,
+                     int32_t top_k, int32_t sigmoid, const float* bias, int32_t groups,
+                     int32_t top_groups, int32_t group_best, int32_t renormalize, float scale,
+                     const uint8_t* w13_codes, const float* w13_scales, int64_t F,
+                     const uint8_t* w2_codes, const float* w2_scales, int rows_dtype, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * w4a4_linear for callers that cannot allocate device memory (code under
  * HIP graph capture, tight serving loops, harnesses that forbid hipMalloc):
  * the same arguments without the workspace, and the same kernels, which work
