@@ -313,7 +313,7 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8GemmArgs& a, const v4f (&a
 // [wm][wn][row]); the stores are range-checked.
 template <int BM, bool BIAS>
 __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[BM / 32][4], int64_t m0, int rows, int tn,
-                                              int wm, int wn, int j, int q, int e, uint32_t (*top)[4][BM / 2])
+                                              int wm, int wn, int j, int q, int e, uint32_t* top)
 {
     constexpr int MT = BM / 32;
     const int64_t F = a.N >> 1;
@@ -342,16 +342,16 @@ __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[B
         }
         m = max(m, (uint32_t)__shfl_xor((int)m, 16));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-        if (q == 0) top[wm][wn][16 * mt + j] = m;
+        if (q == 0) top[(wm * 4 + wn) * (BM / 2) + 16 * mt + j] = m;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        uint32_t m = top[wm][0][16 * mt + j];
+        uint32_t m = top[wm * 4 * (BM / 2) + 16 * mt + j];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) m = max(m, top[wm][w][16 * mt + j]);
+        for (int w = 1; w < 4; ++w) m = max(m, top[(wm * 4 + w) * (BM / 2) + 16 * mt + j]);
         const Fp8Block b = fp8_block(m);
         v2u c;
 #pragma unroll
@@ -393,8 +393,10 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     constexpr int DMAS = AI + 4 + 1;          // all of a step's, per wave
     constexpr int D1 = AI + 1;                // of them with the last row tile; the others follow
     constexpr int PUTS = 2 * MT;              // stores of an epilogue, at least
-    __shared__ __align__(16) uint8_t smem[SLOTS * SLOT];
-    __shared__ uint32_t top[GATED ? 2 : 1][4][GATED ? BM / 2 : 1];
+    // (one array: with several the compiler waits for all DMA before every read)
+    constexpr int TILES = SLOTS * SLOT, TOP = TILES + 2048;
+    __shared__ __align__(16) uint8_t smem[TOP + (GATED ? 2 * 4 * (BM / 2) * 4 : 0)];
+    v4i* const tiles = (v4i*)(smem + TILES);
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -417,10 +419,12 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     } else {
         ntiles = tiles_m * tiles_n;
     }
-    // Lane i of every wave holds the workgroup's i-th tile of a batch of 64.
-    Tile mine;
+    // The workgroup's tiles lie in LDS, two batches of 64: looking one up where it is
+    // needed, in the K loop, would take registers and time that the MFMAs want.  Wave 0
+    // fills a batch.
     auto fill = [&](int batch) {
-        mine = Tile{0, 0, 0, 0};
+        if (wave != 0) return;
+        Tile mine{0, 0, 0, 0};
         const int64_t at = blockIdx.x + (int64_t)(batch * 64 + lane) * gridDim.x;
         const bool have = at < ntiles;
         // each XCD (workgroup index modulo 8; the grid is a multiple of 8 or
@@ -437,16 +441,16 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             mine.tn = in_g / gm;
             mine.rows = have ? (int)min(a.M - mine.m0, (int64_t)BM) : 0;
         }
+        tiles[(batch & 1) * 64 + lane] = (v4i){mine.m0, mine.rows, mine.tn, mine.e};
     };
     auto tile_of = [&](int i) {
-        if (i && !(i & 63)) fill(i >> 6);
-        const int l = i & 63;
-        return Tile{__builtin_amdgcn_readlane(mine.m0, l), __builtin_amdgcn_readlane(mine.rows, l),
-                    __builtin_amdgcn_readlane(mine.tn, l), __builtin_amdgcn_readlane(mine.e, l)};
+        const v4i v = tiles[i & 127];
+        return Tile{__builtin_amdgcn_readfirstlane(v[0]), __builtin_amdgcn_readfirstlane(v[1]),
+                    __builtin_amdgcn_readfirstlane(v[2]), __builtin_amdgcn_readfirstlane(v[3])};
     };
 
     // ---- DMA: wave w moves rows [w BM/8, (w + 1) BM/8) of A and 32 weight columns
-    const int l8 = lane >> 3, ar0 = wave * (BM / 8);
+    const int ar0 = wave * (BM / 8);
     const int ch = (lane & 7) ^ (lane >> 4);   // chunk of this lane; bit 2 of the LDS row's half turns it into ch ^ 4
     const bool gather = GROUPED && a.rows != nullptr;
     // Every resource is 2^31 bytes long: a lane that has nothing to read (a row
@@ -456,18 +460,26 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     int sstep = 0;                   // bytes from a step's scales to the next's
     __amdgpu_buffer_rsrc_t ra, rb, rs;
     auto a_half = [&](int i) { return BM == 64 ? wave & 1 : i & 1; };   // whether A's instruction i takes ch ^ 4
+    // (the lane index, made anew: what depends on it would otherwise be kept in
+    // registers from tile to tile)
+    auto fresh = [&]() {
+        int l = threadIdx.x & 63;
+        asm volatile("" : "+v"(l));
+        return l;
+    };
     auto set_dma = [&](const Tile& t) {
+        const int lane = fresh(), l8 = lane >> 3, ch = (lane & 7) ^ (lane >> 4);
         // the source row of tile row i, or none
-        auto src_row = [&](int i) -> int64_t {
+        auto src_row = [&](int i) -> int {
             if (i >= t.rows) return -1;
             if (!gather) return i;
-            const int64_t s = a.rows[(int64_t)t.m0 + i];
+            const int s = a.rows[(int64_t)t.m0 + i];
             return s >= 0 && s < a.M ? s : -1;
         };
 #pragma unroll
         for (int i = 0; i < AI; ++i) {
-            const int64_t s = src_row(ar0 + 8 * i + l8);
-            avo[i] = s < 0 ? kOut : (uint32_t)(s * K + (ch ^ (a_half(i) * 4)) * 16);
+            const int s = src_row(ar0 + 8 * i + l8);
+            avo[i] = s < 0 ? kOut : (uint32_t)s * (uint32_t)K + (ch ^ (a_half(i) * 4)) * 16;
         }
         ra = mx_rsrc(mx_uniform(gather ? a.a : a.a + (int64_t)t.m0 * K), kOut);
         // LDS rows 32 wave + 8 i + l8: column tile nt, row idx of it
@@ -484,8 +496,8 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
         rb = mx_rsrc(mx_uniform(a.b + (t.rows ? brow : 0) * K), kOut);
         // scales: of 64 rows, or of the two weight blocks
         if (wave < BM / 64) {
-            const int64_t s = src_row(wave * 64 + lane);
-            svo = s < 0 ? kOut : (uint32_t)(s * 4);
+            const int s = src_row(wave * 64 + lane);
+            svo = s < 0 ? kOut : (uint32_t)s * 4;
             rs = mx_rsrc(mx_uniform((const uint8_t*)(gather ? a.sa : a.sa + t.m0)), kOut);
             sstep = (int)(a.M * 4);
         } else {
@@ -524,26 +536,15 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     // The steps of all tiles form one sequence; the DMA runs SLOTS steps, so up
     // to as many tiles, ahead of the MFMAs.
     fill(0);
-    Tile cur = tile_of(0), q0{0, 0, 0, 0}, q1 = q0, q2 = q0;
+    __syncthreads();
+    Tile cur = tile_of(0);
     if (cur.rows == 0) return;
-    int t_dma = 0, s_dma = 0, ahead = 0;
+    int t_cur = 0, t_dma = 0, s_dma = 0;
     set_dma(cur);
     auto advance = [&]() {
         if (++s_dma < nsteps) return;
         s_dma = 0;
-        const Tile t = tile_of(++t_dma);
-        set_dma(t);
-        // (by value: a choice of addresses would put the queue in memory)
-        auto put = [&](Tile& x, bool here) {
-            x.m0 = here ? t.m0 : x.m0;
-            x.rows = here ? t.rows : x.rows;
-            x.tn = here ? t.tn : x.tn;
-            x.e = here ? t.e : x.e;
-        };
-        put(q0, ahead == 0);
-        put(q1, ahead == 1);
-        if constexpr (SLOTS == 3) put(q2, ahead == 2);
-        ++ahead;
+        set_dma(tile_of(++t_dma));
     };
 
     // ---- fragments: LDS rows ao + 16 mt and bo + 16 nt, chunks q and q + 4
@@ -652,6 +653,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
 #pragma unroll
                         for (int x = n * D1 / NT; x < (n + 1) * D1 / NT; ++x) dma(d, sl, x);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                     join_in(i >= 3 ? i - 3 : MT * NT - 3 + i);
                     if (m == 0) {
                         // the rest of the DMA that the step before began (a tile's
@@ -679,10 +681,10 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
         for (int i = MT * NT - 3; i < MT * NT; ++i) join_in(i);
 
         // ---- epilogue
-        const int row0 = wm * (BM / 2) + j;
+        const int l = fresh(), j = l & 15, q = l >> 4, row0 = wm * (BM / 2) + j;
         if constexpr (GATED) {
-            if (a.bias) fp8_put_gated<BM, true>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, top);
-            else fp8_put_gated<BM, false>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, top);
+            if (a.bias) fp8_put_gated<BM, true>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, (uint32_t*)(smem + TOP));
+            else fp8_put_gated<BM, false>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, (uint32_t*)(smem + TOP));
         } else {
             const int64_t n0 = (int64_t)cur.tn * 256;
             const int c0 = wn * 64 + 16 * q;
@@ -691,10 +693,9 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             else fp8_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
         }
         stores = SLOTS - 1;
-        cur = q0;
-        q0 = q1;
-        if constexpr (SLOTS == 3) q1 = q2;
-        --ahead;
+        // (the other batch is read from 29 tiles on at the earliest, many barriers later)
+        if ((++t_cur & 63) == 32) fill((t_cur >> 6) + 1);
+        cur = tile_of(t_cur);
         if (cur.rows == 0) break;
     }
 }
