@@ -365,17 +365,20 @@ __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[B
 // BM x 256 outputs per workgroup of eight waves (2 x 4, each BM/2 x 64, two to a
 // SIMD: with one wave the matrix core would wait for the fmas that read its results),
 // K in steps of 128, a scale block; one workgroup per CU, which takes tiles in turn.
-//   * A step's codes (128 bytes a row) and scales go global -> LDS by DMA into one of
-//     two or three slots, as many steps ahead of their use and, at a tile's end, into
-//     the next tiles' steps.  16-byte chunk c of LDS row r sits at c ^ ((r >> 1) & 7):
-//     a ds_read_b128 serves sixteen lanes a cycle (lanes {0-3, 12-15} of one group of
+//   * A step's codes (128 bytes a row) go global -> LDS by DMA into one of two or three
+//     slots, its scales into one more slot of their own, and at a tile's end those of
+//     the next tiles' steps.  16-byte chunk c of LDS row r sits at c ^ ((r >> 1) & 7): a
+//     ds_read_b128 serves sixteen lanes a cycle (lanes {0-3, 12-15} of one group of
 //     sixteen and {4-11} of its neighbour), and these then hit sixteen different
 //     16-byte bank groups.
 //   * A wave holds all its weight fragments of a step (four column tiles) and walks
-//     the row tiles, whose fragments are read one tile ahead.  Before the last row
-//     tile the waves wait for the next step's DMA and meet: then nobody reads this
-//     step's slot any more, and the DMA furthest ahead goes out into it.  The next
-//     step's weight fragments replace this one's as the last MFMAs let go of them.
+//     the row tiles, whose fragments are read one tile ahead.  Before every fourth row
+//     tile the waves wait for what the next two need and meet: then nobody reads the
+//     last two's rows any more (before the second: nor the weights), and the DMA of the
+//     step that takes this slot next goes out into them.  So LDS holds nearly two steps
+//     in flight (refilled a whole slot at a time, one: 8192 x 8192 x 8192 of zeros, where
+//     power does not matter, ran at 2.9 PFLOP/s, waiting for DMA).  The next step's
+//     weight fragments replace this one's as the last MFMAs let go of them.
 //   * An MFMA's result joins the accumulators three MFMAs later.
 //   * LDS row 16 nt + i of a wave's 64 columns is column 16 (i >> 2) + 4 nt + (i & 3),
 //     so a lane ends with sixteen consecutive columns of one row.  Gated: a wave has
@@ -385,16 +388,18 @@ template <int BM, bool GROUPED, bool GATED, bool HALF>
 __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int tiles_m, int tiles_n)
 {
     constexpr int MT = BM / 32, NT = 4, G = GATED ? 2 : 1;
-    // a slot: codes of both operands, scales of the rows, of the two weight blocks,
-    // and room for the scale DMA of waves that have none, so that all issue the same
-    constexpr int AB = BM * 128, BB = 256 * 128, SA = BM * 4, SLOT = AB + BB + SA + 512;
+    constexpr int AB = BM * 128, SLOT = AB + 256 * 128;   // a slot: codes of both operands
     constexpr int SLOTS = BM == 256 ? 2 : 3;  // what LDS holds
-    constexpr int AI = BM / 64;               // A DMA instructions per wave (8 rows each)
-    constexpr int DMAS = AI + 4 + 1;          // all of a step's, per wave
-    constexpr int D1 = AI + 1;                // of them with the last row tile; the others follow
+    // a scale slot: of the rows, of the two weight blocks, and room for the DMA of
+    // waves that have no scales, so that all issue the same
+    constexpr int SA = BM * 4, SSLOT = SA + 512, S0 = SLOTS * SLOT, SEND = S0 + (SLOTS + 1) * SSLOT;
+    // A step's DMA goes out in NP groups, group k before the last of row tiles PH k ..
+    // PH (k + 1) - 1: their rows, and with the first one the weights and scales.
+    constexpr int PH = MT < 4 ? MT : 4, NP = MT / PH;
+    constexpr int AG = PH / 2, G0 = AG + 5, D = G0 + (NP - 1) * AG;   // instructions per wave: of a group's rows, in all
     constexpr int PUTS = 2 * MT;              // stores of an epilogue, at least
     // (one array: with several the compiler waits for all DMA before every read)
-    constexpr int TILES = SLOTS * SLOT, TOP = TILES + 2048;
+    constexpr int TILES = SEND, TOP = TILES + 2048;
     __shared__ __align__(16) uint8_t smem[TOP + (GATED ? 2 * 4 * (BM / 2) * 4 : 0)];
     v4i* const tiles = (v4i*)(smem + TILES);
 
@@ -449,17 +454,17 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
                     __builtin_amdgcn_readfirstlane(v[2]), __builtin_amdgcn_readfirstlane(v[3])};
     };
 
-    // ---- DMA: wave w moves rows [w BM/8, (w + 1) BM/8) of A and 32 weight columns
-    const int ar0 = wave * (BM / 8);
+    // ---- DMA: wave w moves 8 rows of A at a time, LDS rows (w >> 2) BM/2 + 32 i +
+    // 8 (w & 3) + ..., and 32 weight columns
+    const int ar0 = (wave >> 2) * (BM / 2) + 8 * (wave & 3), ahalf = wave & 1;
     const int ch = (lane & 7) ^ (lane >> 4);   // chunk of this lane; bit 2 of the LDS row's half turns it into ch ^ 4
     const bool gather = GROUPED && a.rows != nullptr;
     // Every resource is 2^31 bytes long: a lane that has nothing to read (a row
     // or column past the tile's, no tile, a chunk past K) has an offset past
     // that and gets zeros.
-    uint32_t avo[AI], bvo[4], svo;   // lane offsets of codes and scales
+    uint32_t avo[MT / 2], bvo[4], svo;   // lane offsets of codes and scales
     int sstep = 0;                   // bytes from a step's scales to the next's
     __amdgpu_buffer_rsrc_t ra, rb, rs;
-    auto a_half = [&](int i) { return BM == 64 ? wave & 1 : i & 1; };   // whether A's instruction i takes ch ^ 4
     // (the lane index, made anew: what depends on it would otherwise be kept in
     // registers from tile to tile)
     auto fresh = [&]() {
@@ -477,9 +482,9 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             return s >= 0 && s < a.M ? s : -1;
         };
 #pragma unroll
-        for (int i = 0; i < AI; ++i) {
-            const int s = src_row(ar0 + 8 * i + l8);
-            avo[i] = s < 0 ? kOut : (uint32_t)s * (uint32_t)K + (ch ^ (a_half(i) * 4)) * 16;
+        for (int i = 0; i < MT / 2; ++i) {
+            const int s = src_row(ar0 + 32 * i + l8);
+            avo[i] = s < 0 ? kOut : (uint32_t)s * (uint32_t)K + (ch ^ (ahalf * 4)) * 16;
         }
         ra = mx_rsrc(mx_uniform(gather ? a.a : a.a + (int64_t)t.m0 * K), kOut);
         // LDS rows 32 wave + 8 i + l8: column tile nt, row idx of it
@@ -508,8 +513,8 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             sstep = 4;
         }
     };
-    // the scale DMA's place in a slot
-    const int sdst = AB + BB + (wave < BM / 64 ? wave * 256 : wave == BM / 64 ? SA : SA + 256);
+    // the scale DMA's place in a scale slot
+    const int sdst = S0 + (wave < BM / 64 ? wave * 256 : wave == BM / 64 ? SA : SA + 256);
 
     // The DMA of one step, an instruction at a time: `Dma` holds what its
     // instructions share.
@@ -521,15 +526,17 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
         d.t0 = s * 8 < chunks - ch ? 0u : kOut;
         d.t1 = s * 8 < chunks - (ch ^ 4) ? 0u : kOut;
         d.ko = s * 128;
-        d.so = s * sstep;
+        d.so = __builtin_amdgcn_readfirstlane(s * sstep);
     };
-    auto dma = [&](const Dma& d, int sl, int n) {
-        if (n < AI) {
-            mx_dma<16>(ra, smem + sl + (ar0 + 8 * n) * 128, avo[n < AI ? n : 0] | (a_half(n) ? d.t1 : d.t0), d.ko);
-        } else if (n == AI) {
-            mx_dma<4>(rs, smem + sl + sdst, svo, d.so);
+    // instruction n of group k, into slot sl and scale slot ssl
+    auto dma = [&](const Dma& d, int sl, int ssl, int k, int n) {
+        if (n < AG) {
+            const int i = k * AG + n;
+            mx_dma<16>(ra, smem + sl + (ar0 + 32 * i) * 128, avo[i] | (ahalf ? d.t1 : d.t0), d.ko);
+        } else if (n == AG) {
+            mx_dma<4>(rs, smem + ssl + sdst, svo, d.so);
         } else {
-            const int i = n - AI - 1;
+            const int i = n - AG - 1;
             mx_dma<16>(rb, smem + sl + AB + (wave * 32 + 8 * i) * 128, bvo[i & 3] | ((i & 1) ? d.t1 : d.t0), d.ko);
         }
     };
@@ -550,7 +557,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     // ---- fragments: LDS rows ao + 16 mt and bo + 16 nt, chunks q and q + 4
     const int sw = (q ^ ((j >> 1) & 7)) * 16;
     const int ao = (wm * (BM / 2) + j) * 128 + sw, bo = AB + (wn * 64 + j) * 128 + sw;
-    const int sao = AB + BB + (wm * (BM / 2) + j) * 4, sbo = AB + BB + SA + (GATED ? 0 : (wn >> 1) * 4);
+    const int sao = S0 + (wm * (BM / 2) + j) * 4, sbo = S0 + SA + (GATED ? 0 : (wn >> 1) * 4);
     v8i fa[2], fb[NT];
     float sa[2], sb[G];
     // (base: a lane's address in a slot, off: the row tile's, which is an immediate)
@@ -559,13 +566,13 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
         f = join(lo, hi);
     };
     // row tile mt of a slot: its fragment and scales
-    auto read_a = [&](int sl, int mt) {
+    auto read_a = [&](int sl, int ssl, int mt) {
         read(fa[mt & 1], sl + ao, mt * 16 * 128);
-        sa[mt & 1] = *(const float*)(smem + sl + sao + mt * 64);
+        sa[mt & 1] = *(const float*)(smem + ssl + sao + mt * 64);
     };
-    auto read_sb = [&](int sl) {
+    auto read_sb = [&](int ssl) {
 #pragma unroll
-        for (int i = 0; i < G; ++i) sb[i] = *(const float*)(smem + sl + sbo + 4 * i);
+        for (int i = 0; i < G; ++i) sb[i] = *(const float*)(smem + ssl + sbo + 4 * i);
     };
 
     Dma d;
@@ -573,17 +580,20 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     for (int s = 0; s < SLOTS; ++s) {
         dma_of(d, s_dma);
 #pragma unroll
-        for (int n = 0; n < DMAS; ++n) dma(d, s * SLOT, n);
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int n = 0; n < (k ? AG : G0); ++n) dma(d, s * SLOT, s * SSLOT, k, n);
         if (s + 1 < SLOTS) advance();
     }
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((SLOTS - 1) * DMAS) : "memory");   // the first step has landed
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(SLOTS * D - G0) : "memory");   // the first group has landed
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int n = 0; n < NT; ++n) read(fb[n], bo, n * 16 * 128);
-    read_a(0, 0);
+    read_a(0, 0, 0);
     read_sb(0);
-    int sl = 0, stores = 0;                // stores: steps in which the last epilogue's may be in flight
+    int sl = 0, ssl = 0;                   // this step's slots
+    int stores = 0;                        // meetings at which the last epilogue's stores may be in flight
     for (;;) {
         v4f acc[MT][NT], tmp[4];
         float f[2][G];                     // factors of a row tile, and of the one before
@@ -603,11 +613,10 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(tmp[i & 3][r], x, c[r]);
             asm volatile("" : "+v"(c));   // here, not behind the next branch
         };
-        int behind = 0;   // the step before has DMA left to send
 #pragma clang loop unroll(disable)
         for (int s = 0; s < nsteps; ++s) {
             const int nx = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
-            asm volatile("" : "+s"(behind));
+            const int snx = ssl == SLOTS * SSLOT ? 0 : ssl + SSLOT, spv = ssl == 0 ? SLOTS * SSLOT : ssl - SSLOT;
             v8h hb[HALF ? NT : 1][4], ha[4];
             if constexpr (HALF) {
 #pragma unroll
@@ -615,11 +624,12 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                if (m == MT - 1) {
-                    // The next step has landed, and this one is read.  Still in flight
-                    // may be the DMA of the steps after the next and, in a tile's first
-                    // SLOTS - 1 steps, the stores of the tile before, which went out
-                    // after it.
+                if (m % PH == PH - 1) {
+                    // What the next PH row tiles need has landed, and the last are read.  Still in flight may be all groups sent since and, until
+                    // they are those that followed them, the stores of the tile before.
+                    constexpr int kAll = SLOTS * D;
+                    const int k = m / PH;
+                    const int n0 = kAll - (k == 0 ? G0 : AG) - ((k + 1) % NP == 0 ? G0 : AG);
                     asm volatile("s_waitcnt lgkmcnt(0)\n\t"
                                  "s_cmp_lt_i32 %0, 1\n\t"
                                  "s_cbranch_scc1 1f\n\t"
@@ -627,8 +637,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
                                  "s_branch 2f\n"
                                  "1:\n\t"
                                  "s_waitcnt vmcnt(%2)\n"
-                                 "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"((SLOTS - 2) * DMAS + PUTS),
-                                 "n"((SLOTS - 2) * DMAS)
+                                 "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"(n0 + PUTS), "n"(n0)
                                  : "memory", "scc");
                     --stores;
                     __builtin_amdgcn_s_barrier();
@@ -644,39 +653,30 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
                     if constexpr (HALF) tmp[i & 3] = f16_mfma(hb[n], ha);
                     else tmp[i & 3] = fp8_mfma(fb[n], fa[m & 1]);
                     if (m < MT - 1) {
-                        if (n == 0) read_a(sl, m + 1);
+                        if (n == 0) read_a(sl, ssl, m + 1);
                     } else {
                         // (past the last step: of a slot's older contents, unused)
-                        if (n == 0) read_a(nx, 0);
+                        if (n == 0) read_a(nx, snx, 0);
                         read(fb[n], nx + bo, n * 16 * 128);
-                        if (n == NT - 1) read_sb(nx);
+                        if (n == NT - 1) read_sb(snx);
+                    }
+                    if (m % PH == PH - 1) {
+                        const int size = m / PH == 0 ? G0 : AG;
 #pragma unroll
-                        for (int x = n * D1 / NT; x < (n + 1) * D1 / NT; ++x) dma(d, sl, x);
+                        for (int x = n * size / NT; x < (n + 1) * size / NT; ++x) dma(d, sl, spv, m / PH, x);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                     join_in(i >= 3 ? i - 3 : MT * NT - 3 + i);
-                    if (m == 0) {
-                        // the rest of the DMA that the step before began (a tile's
-                        // first step: it went out before the epilogue)
-                        if (n == 0 && behind) {
-                            const int pv = sl == 0 ? (SLOTS - 1) * SLOT : sl - SLOT;
-#pragma unroll
-                            for (int x = D1; x < DMAS; ++x) dma(d, pv, x);
-                        }
-                        if (n == 2) {
-                            advance();
-                            dma_of(d, s_dma);
-                        }
+                    if (m == 0 && n == 2) {
+                        advance();
+                        dma_of(d, s_dma);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            behind = 1;
             sl = nx;
+            ssl = snx;
         }
-        const int pv = sl == 0 ? (SLOTS - 1) * SLOT : sl - SLOT;
-#pragma unroll
-        for (int x = D1; x < DMAS; ++x) dma(d, pv, x);
 #pragma unroll
         for (int i = MT * NT - 3; i < MT * NT; ++i) join_in(i);
 
@@ -692,7 +692,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             else if (a.out_dtype == BF16) fp8_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else fp8_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
         }
-        stores = SLOTS - 1;
+        stores = SLOTS * NP - 1;
         // (the other batch is read from 29 tiles on at the earliest, many barriers later)
         if ((++t_cur & 63) == 32) fill((t_cur >> 6) + 1);
         cur = tile_of(t_cur);
