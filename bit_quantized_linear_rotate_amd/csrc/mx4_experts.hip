@@ -14,6 +14,8 @@
 // is one launch, more are two, since the sort needs all chunks' counts.  Measured: 32 tokens of 32 experts, 4
 // choices 3.8 us; 8192 of 128, 8 choices 8.7 + 6.4 us; 8192 of 32, 4 choices
 // 4.9 + 6.6 us.
+#include <type_traits>
+
 #include "common.hpp"
 #include "mx4.hpp"
 
@@ -165,17 +167,17 @@ __device__ __forceinline__ void scan_experts(const int* tot, int* off, int E)
 // which then sorts its own slots.
 template <bool ONE> __device__ __forceinline__ void route_chunk_done(const RouteArgs& a, int* cnt, int* off)
 {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, threads = blockDim.x;
     if constexpr (ONE) {
         scan_experts(cnt, off, a.E);
         __syncthreads();
         const int total = off[a.E];
-        for (int e = tid; e <= a.E; e += 1024) a.offsets[e] = off[e];
-        for (int64_t i = total + tid; i < a.T * a.k; i += 1024) a.rows[i] = -1;
+        for (int e = tid; e <= a.E; e += threads) a.offsets[e] = off[e];
+        for (int64_t i = total + tid; i < a.T * a.k; i += threads) a.rows[i] = -1;
         __syncthreads();
         place_slots(a, 0, a.T * a.k, off);
     } else {
-        for (int e = tid; e < a.E; e += 1024) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+        for (int e = tid; e < a.E; e += threads) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
     }
 }
 
@@ -204,10 +206,13 @@ template <int DT, int L, int NV, bool ONE> __global__ __launch_bounds__(1024) vo
 }
 
 // ---- routing by scores -------------------------------------------------------
-// The choice is made in double precision: in fp32 the rounding of a score would
+// The choice is that of double precision: in fp32 the rounding of a score would
 // decide between experts whose choice values differ by a few parts in 2^24, which a
-// batch of some thousand tokens holds.  Without a bias the scores' order is the
-// logits'.
+// batch of some thousand tokens holds.  A token is first chosen in fp32, by sixteen
+// lanes; where two values that the choice compares lie within the error of that, a
+// wave chooses it again in double precision.  Without a bias the scores' order is the
+// logits', and (unless groups are ranked by sums) nothing is in doubt.  The weights
+// are computed in double precision, a choice to a lane.
 
 // the value of the lane whose index differs in bits D, for the lanes of one token
 template <int L> __device__ __forceinline__ double lanes_max64(double v)
@@ -243,14 +248,15 @@ __device__ __forceinline__ void route_scored_token(const RouteScoredArgs& a, int
     const double none = -__builtin_inf();
     const int e0 = lane * NV;
     double score[NV], val[NV];
-    float top = -__builtin_inff();
+    float logit[NV], top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = e0 + i;
         // (+ 0: both zeros are the same logit; a NaN is no logit)
         const float l = live && e < a.E ? add_rn(load_any_f32(a.dtype, a.logits, t * a.stride + e), 0.0f) : -__builtin_inff();
-        val[i] = l > -__builtin_inff() ? (double)l : none;
-        top = fmaxf(top, (float)val[i]);
+        logit[i] = l > -__builtin_inff() ? l : -__builtin_inff();
+        val[i] = (double)logit[i];
+        top = fmaxf(top, logit[i]);
     }
     if (a.sigmoid) {
 #pragma unroll
@@ -272,15 +278,15 @@ __device__ __forceinline__ void route_scored_token(const RouteScoredArgs& a, int
     if (a.bias) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const double v = score[i] + (double)(e0 + i < a.E ? a.bias[e0 + i] : 0.0f);
+            const double v = score[i] + (double)a.bias[min(e0 + i, a.E - 1)];
             val[i] = val[i] > none && v > none ? v : none;
         }
     }
     if constexpr (GROUPS) {
         const int size = a.E / a.groups;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (e0 + i < a.E) worth[e0 + i] = val[i] > none ? (a.bias ? val[i] : score[i]) : none;
+        for (int i = 0; i < NV; ++i)   // (without a bias the largest is known by its logit)
+            if (e0 + i < a.E) worth[e0 + i] = val[i] > none && !a.bias && a.group_best == 2 ? score[i] : val[i];
         __threadfence_block();
         __builtin_amdgcn_wave_barrier();
         constexpr int GN = kRouteMaxGroups / L;   // groups of a lane, neighbours
@@ -363,25 +369,313 @@ __device__ __forceinline__ void route_scored_token(const RouteScoredArgs& a, int
     weight = (float)(mine * (double)a.scale);
 }
 
-template <int L, int NV, bool GROUPS, bool ONE>
-__global__ __launch_bounds__(1024) void route_scored_kernel(RouteScoredArgs a, int64_t chunk)
+template <int L> __device__ __forceinline__ float lanes_maxf(float v)
 {
+    auto step = [&](auto ctrl) {
+        const int b = __float_as_int(v);
+        v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, decltype(ctrl)::value, 0xf, 0xf, false)));
+    };
+    if constexpr (L == 16) {
+        step(std::integral_constant<int, 0x128>());   // row_ror 8, 4, 2, 1
+        step(std::integral_constant<int, 0x124>());
+        step(std::integral_constant<int, 0x122>());
+        step(std::integral_constant<int, 0x121>());
+        return v;
+    }
+    step(std::integral_constant<int, 0x111>());   // row_shr 1, 2, 4, 8
+    step(std::integral_constant<int, 0x112>());
+    step(std::integral_constant<int, 0x114>());
+    step(std::integral_constant<int, 0x118>());
+    step(std::integral_constant<int, 0x142>());   // row_bcast 15, 31
+    step(std::integral_constant<int, 0x143>());
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Keys of N values per lane, of which the largest over L lanes tells the largest value
+// and its index (i L + lane), the lower of equals: the index in the last BITS bits,
+// above it the value.  16-bit values (exact) fit as they are; others in fixed point
+// between the token's smallest and largest.  Then values `apart` units and less from
+// one another may be in either order: error (of their difference), and a unit each for
+// the difference, the product and the cut, of either.
+template <int L, int N, int BITS> struct Ranked {
+    uint32_t key[N];
+    uint32_t apart = 0;
+    bool exact;
+    __device__ __forceinline__ void set(const float (&v)[N], bool exact_, float error, int lane)
+    {
+        constexpr uint32_t low = (1u << BITS) - 1;
+        const float none = -__builtin_inff();
+        exact = exact_;
+        float lo = __builtin_inff(), hi = none;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            hi = fmaxf(hi, v[i]);
+            lo = fminf(lo, v[i] > none ? v[i] : lo);
+        }
+        hi = lanes_maxf<L>(hi);
+        lo = -lanes_maxf<L>(-lo);
+        const float range = add_rn(hi, -lo);
+        float unit = ((float)(1u << (32 - BITS)) - 512.0f) / range;
+        if (!exact && hi > none) {
+            // (a range of zero or infinity: nothing is told apart)
+            if (!(unit < 0x1p120f && unit > 0.0f)) unit = 0.0f;
+            apart = (uint32_t)fminf(__builtin_fmaf(error, unit, 6.0f), 0x1p31f);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t b = __float_as_uint(v[i]), order = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+            const uint32_t at = low - (uint32_t)(i * L + lane);
+            const uint32_t fixed = ((uint32_t)mul_rn(add_rn(v[i], -lo), unit) + 1) << BITS;
+            key[i] = v[i] > none ? (exact ? order & ~low : fixed) | at : 0;
+        }
+    }
+    // The next largest's key, 0: none.
+    __device__ __forceinline__ uint32_t next()
+    {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) best = max(best, key[i]);
+        best = lanes_max<L>(best);
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = key[i] == best ? 0 : key[i];
+        return best;
+    }
+    static __device__ __forceinline__ int index(uint32_t k)
+    {
+        constexpr uint32_t low = (1u << BITS) - 1;
+        return k ? (int)(low - (k & low)) : -1;
+    }
+    // whether the later of two keys may belong before the earlier one
+    __device__ __forceinline__ bool doubt(uint32_t earlier, uint32_t later) const
+    {
+        return !exact && later && (earlier >> BITS) - (later >> BITS) <= apart;
+    }
+};
+
+// One token in fp32 by L lanes, NV consecutive experts each: choice r ends in lane r
+// (worth: its E values in LDS, sixteen and a gap each time, GROUPS only).
+// unsure: two values that decide who is chosen lie within their error.  exp(x) is off by
+// (1.5 |x| + 2) 2^-24 of itself (two roundings of its argument in base 2, the power),
+// 1 / (1 + exp(-l)) by s (1 - s) times that, at most 0.53 2^-24, or where all logits are
+// below zero (1.5 |l| + 2) 2^-24 of itself, and 3 2^-24 of itself for sum and
+// reciprocal; softmax terms by 3 2^-24 of the largest, their sum by NV + 6 and its
+// reciprocal and the product by 2; the bias adds 2^-24.  With V the largest of all scores
+// and choice values two choice values so differ by 2^-23 (6 + 1.5 |l|) V and 2^-23 (14 +
+// NV) V at most from their true difference, sums of two by twice that.  (2^-119: what
+// the hardware's reciprocal rounds to zero.)
+template <int DT, int L, int NV, bool GROUPS>
+__device__ __forceinline__ void route_quick_token(const RouteScoredArgs& a, int64_t t, bool live, int lane, float* worth,
+                                                  int& expert, float& weight, bool& unsure)
+{
+    const float none = -__builtin_inff();
+    // (made anew for every token: kept from one to the next, what depends on it would
+    // fill registers and a page of instructions ahead of the loop)
+    asm volatile("" : "+v"(lane));
+    float val[NV], top = none;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) val[i] = load_as_f32<DT>(a.logits, (live ? t * a.stride : 0) + min(i * L + lane, a.E - 1));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        // (+ 0: both zeros are the same logit; a NaN is no logit)
+        val[i] = add_rn(val[i], 0.0f);
+        val[i] = live && i * L + lane < a.E && val[i] > none ? val[i] : none;
+        top = fmaxf(top, val[i]);
+    }
+    top = lanes_maxf<L>(top);
+    // scores, where the choice needs them; the sum of the softmax in double precision
+    // where the candidates' values or the weights need it
+    const bool sums = GROUPS && a.group_best == 2, scored = a.bias || sums;
+    float score[NV], error = 0.0f;   // of any choice value that is compared
+    double total = 0.0;
+    if (!a.sigmoid && (a.bias || !a.renormalize)) {
+        // (a loop over memory: exp NV times over would fill the instruction cache)
+#pragma clang loop unroll(disable)
+        for (int i = 0; i < NV; ++i) {
+            const int e = i * L + lane;
+            const float l = live && e < a.E ? load_as_f32<DT>(a.logits, t * a.stride + e) : none;
+            total += l > none ? (l == top ? 1.0 : exp((double)l - (double)top)) : 0.0;
+        }
+        total = lanes_sum64<L>(total);
+    }
+    if (scored) {
+        float sum = 0.0f, largest = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            // (0 of -inf; a NaN where the largest logit is infinite, and then in doubt)
+            if (a.sigmoid) score[i] = __builtin_amdgcn_rcpf(add_rn(1.0f, __expf(-val[i])));
+            else score[i] = __expf(val[i] - top);
+            sum = add_rn(sum, score[i]);
+        }
+        if (!a.sigmoid) {
+            sum = lanes_sum<L>(sum);
+            const float inv = 1.0f / sum;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) score[i] = mul_rn(score[i], inv);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float v = score[i];
+            if (a.bias) {
+                v = add_rn(v, a.bias[min(i * L + lane, a.E - 1)]);
+                val[i] = val[i] > none && v > none ? v : none;   // (a NaN would pass the maxima and minima by)
+                v = fabsf(v) < __builtin_inff() ? fabsf(v) : 0.0f;
+            }
+            largest = fmaxf(largest, fmaxf(score[i], v));
+        }
+        error = __builtin_fmaf(lanes_maxf<L>(largest), (a.sigmoid ? 6.0f - 1.5f * fminf(top, 0.0f) : 14.0f + NV) * 0x1p-23f, 0x1p-119f);
+        unsure = top == __builtin_inff();
+    } else {
+        unsure = false;
+    }
+    constexpr bool narrow = DT != F32;
+    if constexpr (GROUPS) {
+        const int size = a.E / a.groups;
+        auto place = [](int e) { return e + (e >> 4); };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) worth[place(i * L + lane)] = val[i] > none && !a.bias && sums ? score[i] : val[i];
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+        constexpr int GN = kRouteMaxGroups / L;   // groups of a lane, neighbours
+        float of[GN];
+#pragma unroll
+        for (int i = 0; i < GN; ++i) {
+            const int g = i * L + lane;
+            of[i] = none;
+            if (g < a.groups) {
+                float m1 = none, m2 = none;
+                auto take = [&](float v) {
+                    m2 = fmaxf(m2, fminf(m1, v));
+                    m1 = fmaxf(m1, v);
+                };
+                int x = 0;
+                for (; x + 8 <= size; x += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) v[y] = worth[place(g * size + x + y)];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) take(v[y]);
+                }
+                for (; x < size; ++x) take(worth[place(g * size + x)]);
+                of[i] = sums && m2 > none ? add_rn(m1, m2) : m1;
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        Ranked<L, GN, 6> groups;
+        groups.set(of, !scored && narrow, scored ? 2.0f * error : 0.0f, lane);
+        unsigned long long kept = 0;
+        uint32_t last = 0;
+        for (int r = 0; r < a.top_groups; ++r) {
+            last = groups.next();
+            if (last) kept |= 1ull << groups.index(last);
+        }
+        if (groups.doubt(last, groups.next())) unsure = true;
+        // (e + 0.5) / size in fp32 is off an integer by 0.5 / 1024 at least
+        const float inv = 1.0f / (float)size;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int g = (int)(((float)(i * L + lane) + 0.5f) * inv);
+            if (!((kept >> (g & 63)) & 1)) val[i] = none;
+        }
+    }
+    Ranked<L, NV, (L * NV <= 256 ? 8 : 10)> experts;
+    experts.set(val, !a.bias && narrow, a.bias ? error : 0.0f, lane);
+    // Two candidates more than are taken.  What comes after them is in doubt where it
+    // may belong before the last that is taken; the candidates themselves are put in
+    // order by their values in double precision, a candidate to a lane.
+    expert = -1;
+    uint32_t last = 0;
+    for (int r = 0; r < a.k + 2; ++r) {
+        const uint32_t k = experts.next();
+        if (lane == r) expert = experts.index(k);
+        if (r == a.k - 1) last = k;
+        if (r == a.k + 1 && experts.doubt(last, k)) unsure = true;
+    }
+    double s = 0.0, c = -__builtin_inf();
+    if (expert >= 0) {
+        const double l = (double)load_as_f32<DT>(a.logits, t * a.stride + expert) + 0.0;
+        const double x = exp(a.sigmoid ? -l : l - (double)top);
+        s = a.sigmoid ? 1.0 / (1.0 + x) : l == (double)top ? 1.0 : x;
+        c = l;
+        if (a.bias) c = (a.sigmoid ? s : s / total) + (double)a.bias[expert];
+    }
+    auto misplaced = [&]() {   // the next lane's candidate belongs before this one's
+        const double cn = __shfl_down(c, 1);
+        const int en = __shfl_down(expert, 1);
+        return lane <= a.k && en >= 0 && (cn > c || (cn == c && en < expert));
+    };
+    if (!experts.exact && __any(misplaced())) {
+        for (int pass = 0; pass < 2; ++pass) {   // pairs (0, 1), (2, 3), ..; (1, 2), (3, 4), ..
+            const int with = ((lane + pass) ^ 1) - pass;
+            const int from = (threadIdx.x & 63) - lane + max(with, 0);
+            const double co = __shfl(c, from), so = __shfl(s, from);
+            const int eo = __shfl(expert, from);
+            const bool first = with > lane;
+            const bool theirs = eo >= 0 && expert >= 0 && (co > c || (co == c && eo < expert));
+            if (with >= 0 && with <= a.k + 1 && lane <= a.k + 1 && eo >= 0 && expert >= 0 && theirs == first) {
+                c = co;
+                s = so;
+                expert = eo;
+            }
+        }
+        if (misplaced()) unsure = true;
+        // (any lane's doubt is the token's)
+        unsure = lanes_maxf<L>(unsure ? 1.0f : 0.0f) > 0.0f;
+    }
+    if (lane >= a.k) {
+        expert = -1;
+        s = 0.0;
+    }
+    if (a.renormalize) total = lanes_sum64<L>(s);
+    else if (a.sigmoid) total = 1.0;
+    weight = (float)(total > 0.0 ? s / total * (double)a.scale : 0.0);
+}
+
+// (sixteen experts a lane take more than the 128 registers of 1024 threads)
+template <int NV> constexpr int route_scored_threads() { return NV > 8 ? 512 : 1024; }
+
+template <int DT, int L, int NV, bool GROUPS, bool ONE>
+__global__ __launch_bounds__(route_scored_threads<NV>()) void route_scored_kernel(RouteScoredArgs a, int64_t chunk)
+{
+    constexpr int kThreads = route_scored_threads<NV>();
     __shared__ int cnt[kRouteMaxExperts], off[kRouteMaxExperts + 1];
-    __shared__ double worth[GROUPS ? 1024 / L : 1][GROUPS ? L * NV : 1];
-    const int tid = threadIdx.x, lane = tid & (L - 1);
-    for (int e = tid; e < a.E; e += 1024) cnt[e] = 0;
+    constexpr int kInDoubt = -2;   // experts of a token that is to be chosen in double precision
+    __shared__ int doubts;
+    // a wave's: 64 / L tokens in fp32, or one in double precision
+    constexpr int NW = (L * NV + 63) / 64;
+    __shared__ double worth[GROUPS ? kThreads / 64 : 1][GROUPS ? 64 * NW > 34 * NV ? 64 * NW : 34 * NV : 1];
+    const int tid = threadIdx.x, lane = tid & (L - 1), wl = tid & 63;
+    for (int e = tid; e < a.E; e += kThreads) cnt[e] = 0;
+    if (tid == 0) doubts = 0;
     __syncthreads();
     const int64_t t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, a.T);
+    double* const own = worth[GROUPS ? tid >> 6 : 0];
     // (all lanes of a wave stay in the loop: lanes read one another)
-    for (int64_t tw = t0 + (tid >> 6) * (64 / L); tw < t1; tw += 1024 / L) {
-        const int64_t t = tw + ((tid & 63) / L);
+    for (int64_t tw = t0 + (tid >> 6) * (64 / L); tw < t1; tw += kThreads / L) {
+        const int64_t t = tw + wl / L;
         int e;
         float w;
-        route_scored_token<L, NV, GROUPS>(a, t, t < t1, lane, worth[GROUPS ? tid / L : 0], e, w);
+        bool unsure;
+        route_quick_token<DT, L, NV, GROUPS>(a, t, t < t1, lane, (float*)own + (GROUPS ? wl / L * (L * NV * 17 / 16) : 0), e, w, unsure);
+        if (unsure) doubts = 1;
         if (lane < a.k && t < t1) {
             a.weights[t * a.k + lane] = w;
-            a.experts[t * a.k + lane] = e;
-            if (e >= 0) atomicAdd(&cnt[e], 1);
+            a.experts[t * a.k + lane] = unsure ? kInDoubt : e;
+            if (e >= 0 && !unsure) atomicAdd(&cnt[e], 1);
+        }
+    }
+    __syncthreads();
+    if (doubts) {   // a wave to a token
+        for (int64_t t = t0 + (tid >> 6); t < t1; t += kThreads / 64) {
+            if (__builtin_amdgcn_readfirstlane(a.experts[t * a.k]) != kInDoubt) continue;
+            int e, l = wl;
+            float w;
+            asm volatile("" : "+v"(l));
+            route_scored_token<64, NW, GROUPS>(a, t, true, l, own, e, w);
+            if (wl < a.k) {
+                a.weights[t * a.k + wl] = w;
+                a.experts[t * a.k + wl] = e;
+                if (e >= 0) atomicAdd(&cnt[e], 1);
+            }
         }
     }
     __syncthreads();
@@ -425,10 +719,11 @@ __global__ __launch_bounds__(kSortThreads) void route_sort_kernel(RouteArgs a, i
 }
 
 // `kernel` on the chunks of a.T tokens, then, where there is more than one, the sort
-template <class Args> hipError_t route_launch(const Args& a, void (*one)(Args, int64_t), void (*many)(Args, int64_t), hipStream_t st)
+template <class Args>
+hipError_t route_launch(const Args& a, void (*one)(Args, int64_t), void (*many)(Args, int64_t), int threads, hipStream_t st)
 {
     const int64_t chunks = route_chunks(a.T), chunk = (a.T + chunks - 1) / chunks;
-    hipLaunchKernelGGL(chunks == 1 ? one : many, dim3((unsigned)chunks), dim3(1024), 0, st, a, chunk);
+    hipLaunchKernelGGL(chunks == 1 ? one : many, dim3((unsigned)chunks), dim3((unsigned)threads), 0, st, a, chunk);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || chunks == 1) return e;
     hipLaunchKernelGGL(route_sort_kernel, dim3((unsigned)chunks), dim3(kSortThreads), 0, st, a, chunk, (int)chunks);
@@ -437,14 +732,16 @@ template <class Args> hipError_t route_launch(const Args& a, void (*one)(Args, i
 
 template <int DT, int L, int NV> hipError_t route_nv(const RouteArgs& a, hipStream_t st)
 {
-    return route_launch<RouteArgs>(a, route_kernel<DT, L, NV, true>, route_kernel<DT, L, NV, false>, st);
+    return route_launch<RouteArgs>(a, route_kernel<DT, L, NV, true>, route_kernel<DT, L, NV, false>, 1024, st);
 }
 
-template <int L, int NV> hipError_t route_scored_nv(const RouteScoredArgs& a, hipStream_t st)
+template <int DT, int L, int NV> hipError_t route_scored_nv(const RouteScoredArgs& a, hipStream_t st)
 {
     if (a.groups > a.top_groups)
-        return route_launch<RouteScoredArgs>(a, route_scored_kernel<L, NV, true, true>, route_scored_kernel<L, NV, true, false>, st);
-    return route_launch<RouteScoredArgs>(a, route_scored_kernel<L, NV, false, true>, route_scored_kernel<L, NV, false, false>, st);
+        return route_launch<RouteScoredArgs>(a, route_scored_kernel<DT, L, NV, true, true>, route_scored_kernel<DT, L, NV, true, false>,
+                                             route_scored_threads<NV>(), st);
+    return route_launch<RouteScoredArgs>(a, route_scored_kernel<DT, L, NV, false, true>, route_scored_kernel<DT, L, NV, false, false>,
+                                         route_scored_threads<NV>(), st);
 }
 
 template <int DT> hipError_t route_dt(const RouteArgs& a, hipStream_t st)
@@ -455,6 +752,15 @@ template <int DT> hipError_t route_dt(const RouteArgs& a, hipStream_t st)
         return a.E <= 32 ? route_nv<DT, 16, 2>(a, st) : a.E <= 64 ? route_nv<DT, 16, 4>(a, st)
                : a.E <= 128 ? route_nv<DT, 16, 8>(a, st) : route_nv<DT, 16, 16>(a, st);
     return a.E <= 256 ? route_nv<DT, 64, 4>(a, st) : route_nv<DT, 64, 16>(a, st);
+}
+
+template <int DT> hipError_t route_scored_dt(const RouteScoredArgs& a, hipStream_t st)
+{
+    // (the candidates, two more than are taken, have a lane each)
+    if (a.E <= 256 && a.k <= 14)
+        return a.E <= 32 ? route_scored_nv<DT, 16, 2>(a, st) : a.E <= 64 ? route_scored_nv<DT, 16, 4>(a, st)
+               : a.E <= 128 ? route_scored_nv<DT, 16, 8>(a, st) : route_scored_nv<DT, 16, 16>(a, st);
+    return a.E <= 256 ? route_scored_nv<DT, 64, 4>(a, st) : route_scored_nv<DT, 64, 16>(a, st);
 }
 
 // Combining: out[t] = sum_j w[t][j] y[pos[t][j]] in fp32, j in order, rounded
@@ -546,10 +852,12 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st)
 
 hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t st)
 {
-    if (a.E <= 256 && a.k <= 16)
-        return a.E <= 32 ? route_scored_nv<16, 2>(a, st) : a.E <= 64 ? route_scored_nv<16, 4>(a, st)
-               : a.E <= 128 ? route_scored_nv<16, 8>(a, st) : route_scored_nv<16, 16>(a, st);
-    return a.E <= 256 ? route_scored_nv<64, 4>(a, st) : route_scored_nv<64, 16>(a, st);
+    switch (a.dtype) {
+    case F32: return route_scored_dt<F32>(a, st);
+    case F16: return route_scored_dt<F16>(a, st);
+    case BF16: return route_scored_dt<BF16>(a, st);
+    }
+    return hipErrorNotSupported;
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st)

@@ -119,7 +119,8 @@ def route(logits, k, scores="softmax", bias=None, groups=1, top_groups=None, gro
         if top_groups < groups:
             worth = {}
             for g in range(groups):
-                two = sorted((v[e] for e in live if e // size == g), reverse=True)[:group_best]
+                of = l[t] if bias is None and group_best == 1 else v   # the largest is known by its logit
+                two = sorted((of[e] for e in live if e // size == g), reverse=True)[:group_best]
                 if two:
                     worth[g] = sum(two)
             kept = sorted(worth, key=lambda g: (-worth[g], g))[:top_groups]
