@@ -39,25 +39,25 @@ __device__ __forceinline__ v8i join(v4i lo, v4i hi)
     return (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 // The lane's 32 codes as fp16, four operands of the 16x16x32 instruction
-__device__ __forceinline__ void fp8_to_f16(v8i c, v8h (&h)[4])
+typedef int v16i __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ v16i fp8_to_f16(v8i c)
 {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const v2h p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t], 1.0f, false);
-        const v2h p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t], 1.0f, true);
-        const v2h p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t + 1], 1.0f, false);
-        const v2h p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * t + 1], 1.0f, true);
-        h[t] = (v8h){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-    }
+    // (written out: a loop over the elements would put the fragments in memory)
+#define FP8_F16(i) __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[(i) >> 1], 1.0f, (i) & 1))
+    return (v16i){FP8_F16(0), FP8_F16(1), FP8_F16(2), FP8_F16(3), FP8_F16(4), FP8_F16(5), FP8_F16(6), FP8_F16(7),
+                  FP8_F16(8), FP8_F16(9), FP8_F16(10), FP8_F16(11), FP8_F16(12), FP8_F16(13), FP8_F16(14), FP8_F16(15)};
+#undef FP8_F16
 }
-__device__ __forceinline__ v4f f16_mfma(const v8h (&w)[4], const v8h (&a)[4])
+__device__ __forceinline__ v4f f16_mfma(v16i w, v16i a)
 {
+#define FP8_QUARTER(v, t) __builtin_bit_cast(v8h, __builtin_shufflevector(v, v, 4 * t, 4 * t + 1, 4 * t + 2, 4 * t + 3))
     v4f d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < 4; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], a[t], d, 0, 0, 0);
-    return d;
+    d = __builtin_amdgcn_mfma_f32_16x16x32_f16(FP8_QUARTER(w, 0), FP8_QUARTER(a, 0), d, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_16x16x32_f16(FP8_QUARTER(w, 1), FP8_QUARTER(a, 1), d, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_16x16x32_f16(FP8_QUARTER(w, 2), FP8_QUARTER(a, 2), d, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(FP8_QUARTER(w, 3), FP8_QUARTER(a, 3), d, 0, 0, 0);
+#undef FP8_QUARTER
 }
 
 // Zeros for the sorted rows that no expert owns (before offsets[0] and from
@@ -177,10 +177,7 @@ __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
                 for (int nt = 0; nt < NT; ++nt) {
                     v4f p;
                     if constexpr (HALF) {
-                        v8h hb[4], ha[4];
-                        fp8_to_f16(join(fb[u][nt][0], fb[u][nt][1]), hb);
-                        fp8_to_f16(join(fa[u][mt][0], fa[u][mt][1]), ha);
-                        p = f16_mfma(hb, ha);
+                        p = f16_mfma(fp8_to_f16(join(fb[u][nt][0], fb[u][nt][1])), fp8_to_f16(join(fa[u][mt][0], fa[u][mt][1])));
                     } else {
                         p = fp8_mfma(join(fb[u][nt][0], fb[u][nt][1]), join(fa[u][mt][0], fa[u][mt][1]));
                     }
@@ -243,11 +240,11 @@ __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
 }
 
 // ---- the tile kernel ---------------------------------------------------------
-// The epilogue of a wave: rows row0 + 16 mt of the tile, sixteen consecutive
-// columns from n0 + c0 in this lane, as pieces of 16 bytes (the columns of a row
-// need not be aligned to them).  Range-checked buffer stores, so that every wave
-// issues the same number of them whatever the tile holds.  CUT: the piece that the
-// matrix's last column cuts goes out a value at a time.
+// The epilogue of a wave: rows row0 + 16 mt of the tile, columns n0 + c0 .. + 7 and
+// n0 + c0 + 32 .. + 39 in this lane, as pieces of 16 bytes (four lanes: 64 bytes of a
+// row; the columns of a row need not be aligned to them).  Range-checked buffer stores,
+// so that every wave issues the same number of them whatever the tile holds.  CUT: the
+// piece that the matrix's last column cuts goes out a value at a time.
 template <int ODT, int MT, bool BIAS, bool CUT>
 __device__ __forceinline__ void fp8_put(const Fp8GemmArgs& a, const v4f (&acc)[MT][4], int64_t m0, int row0, int rows,
                                         int64_t n0, int c0, int e)
@@ -258,38 +255,48 @@ __device__ __forceinline__ void fp8_put(const Fp8GemmArgs& a, const v4f (&acc)[M
         mx_rsrc(mx_uniform((const uint8_t*)a.out + (m0 * N + n0) * ESZ), ((int64_t)rows * N - n0) * ESZ);
     const uint32_t rstep = (uint32_t)(16 * N * ESZ), off = (uint32_t)((row0 * N + c0) * ESZ);
     const int left = (int)min(N - n0, (int64_t)256) - c0;   // columns from this lane's first
-    float bv[1][16];
-    if constexpr (BIAS) mx_bias<1>(a, e, 0, N, n0 + c0, bv);
+    auto col = [](int i) { return i < 8 ? i : i + 24; };    // of value i
+    float bv[2][16];
+    if constexpr (BIAS) mx_bias<2>(a, e, 0, N, n0 + c0, bv);   // (columns c0 .. + 15 and c0 + 32 .. + 47)
     uint32_t at[P];   // (past the resource, and so with any mt rstep, where the piece is not whole)
 #pragma unroll
-    for (int p = 0; p < P; ++p) at[p] = PIECE * (p + 1) <= left ? off + PIECE * p * ESZ : kOut;
+    for (int p = 0; p < P; ++p) at[p] = col(PIECE * p) + PIECE <= left ? off + col(PIECE * p) * ESZ : kOut;
+    v4f b4[4];
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            b4[i] = (v4f){bv[i >> 1][4 * (i & 1)], bv[i >> 1][4 * (i & 1) + 1], bv[i >> 1][4 * (i & 1) + 2], bv[i >> 1][4 * (i & 1) + 3]};
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] = acc[mt][i >> 2][i & 3];
-            if constexpr (BIAS) v[i] = add_rn(v[i], bv[0][i]);
-        }
+        auto plus = [&](v4f x, int i) {
+            if constexpr (BIAS) x = (v4f){add_rn(x[0], b4[i][0]), add_rn(x[1], b4[i][1]), add_rn(x[2], b4[i][2]), add_rn(x[3], b4[i][3])};
+            return x;
+        };
+        v4f c0_ = plus(acc[mt][0], 0), c1_ = plus(acc[mt][1], 1), c2_ = plus(acc[mt][2], 2), c3_ = plus(acc[mt][3], 3);
+        // (values from here on: a choice among their addresses would put all in memory)
+        asm volatile("" : "+v"(c0_), "+v"(c1_), "+v"(c2_), "+v"(c3_));
+        auto four = [&](int i) { return i == 0 ? c0_ : i == 1 ? c1_ : i == 2 ? c2_ : c3_; };
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             v4u w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (ODT == F32) w[i] = __float_as_uint(v[4 * p + i]);
-                else w[i] = mx_pack2<ODT>(v[8 * p + 2 * i], v[8 * p + 2 * i + 1]);
+            if constexpr (ODT == F32) {
+                w = __builtin_bit_cast(v4u, four(p & 3));
+            } else {
+                const v4f x = four(2 * (p & 1)), y = four(2 * (p & 1) + 1);
+                w = (v4u){mx_pack2<ODT>(x[0], x[1]), mx_pack2<ODT>(x[2], x[3]), mx_pack2<ODT>(y[0], y[1]), mx_pack2<ODT>(y[2], y[3])};
             }
             __builtin_amdgcn_raw_buffer_store_b128(w, ro, (int)(at[p] + mt * rstep), 0, 0);
         }
         if constexpr (CUT) {
-            const int from = left / PIECE * PIECE;   // of these sixteen columns, up to `left`
-            if (row0 + 16 * mt < rows && left > 0 && from < 16) {
+            if (row0 + 16 * mt < rows) {
                 char* o = (char*)a.out + ((m0 + row0 + 16 * mt) * N + n0 + c0) * ESZ;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (i >= from && i < left) store_any(ODT, o, i, v[i]);
+                    if (col(i) < left && col(i / PIECE * PIECE) + PIECE > left) store_any(ODT, o, col(i), four(i >> 2)[i & 3]);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);   // one row tile's values at a time
     }
 }
 
@@ -330,15 +337,17 @@ __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[B
     for (int mt = 0; mt < MT; ++mt) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float g = acc[mt][i >> 2][i & 3], u = acc[mt][2 + (i >> 2)][i & 3];
+        for (int h = 0; h < 2; ++h) {
+            v4f g = acc[mt][h], u = acc[mt][2 + h];
+            asm volatile("" : "+v"(g), "+v"(u));
             if constexpr (BIAS) {
-                g = add_rn(g, bg[0][i]);
-                u = add_rn(u, bu[0][i]);
+                g = (v4f){add_rn(g[0], bg[0][4 * h]), add_rn(g[1], bg[0][4 * h + 1]), add_rn(g[2], bg[0][4 * h + 2]), add_rn(g[3], bg[0][4 * h + 3])};
+                u = (v4f){add_rn(u[0], bu[0][4 * h]), add_rn(u[1], bu[0][4 * h + 1]), add_rn(u[2], bu[0][4 * h + 2]), add_rn(u[3], bu[0][4 * h + 3])};
             }
-            const float v = mx_gated(g, u);
-            acc[mt][i >> 2][i & 3] = v;
-            m = max(m, __float_as_uint(v) & 0x7fffffffu);
+            const v4f v = {mx_gated(g[0], u[0]), mx_gated(g[1], u[1]), mx_gated(g[2], u[2]), mx_gated(g[3], u[3])};
+            acc[mt][h] = v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(v[r]) & 0x7fffffffu);
         }
         m = max(m, (uint32_t)__shfl_xor((int)m, 16));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32));
@@ -380,10 +389,10 @@ __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[B
 //     power does not matter, ran at 2.9 PFLOP/s, waiting for DMA).  The next step's
 //     weight fragments replace this one's as the last MFMAs let go of them.
 //   * An MFMA's result joins the accumulators three MFMAs later.
-//   * LDS row 16 nt + i of a wave's 64 columns is column 16 (i >> 2) + 4 nt + (i & 3),
-//     so a lane ends with sixteen consecutive columns of one row.  Gated: a wave has
-//     32 gates (nt = 0, 1) and the 32 ups that belong to them, eight consecutive of
-//     each in a lane.
+//   * LDS row 16 nt + i of a wave's 64 columns is column 32 (nt >> 1) + 8 (i >> 2) +
+//     4 (nt & 1) + (i & 3), so a lane ends with twice eight consecutive columns of one
+//     row, 64 bytes of it in four lanes.  Gated: with 32 gates (nt = 0, 1) and the 32
+//     ups that belong to them, eight of each in a lane.
 template <int BM, bool GROUPED, bool GATED, bool HALF>
 __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int tiles_m, int tiles_n)
 {
@@ -493,8 +502,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int nt = (wave & 1) * 2 + (i >> 1), idx = (i & 1) * 8 + l8;
-            const int c = GATED ? wn * 32 + 8 * (idx >> 2) + 4 * (nt & 1) + (idx & 3)
-                                : wn * 64 + 16 * (idx >> 2) + 4 * nt + (idx & 3);
+            const int c = (GATED ? wn * 32 : wn * 64 + 32 * (nt >> 1)) + 8 * (idx >> 2) + 4 * (nt & 1) + (idx & 3);
             bvo[i] = col0 + c < ncols ? (uint32_t)(c * (uint32_t)K + (ch ^ ((i & 1) * 4)) * 16) : kOut;
         }
         const int64_t brow = (int64_t)t.e * N + col0 + (GATED && (wave & 1) ? F : 0);
@@ -607,20 +615,22 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
         for (int g = 0; g < G; ++g) f[1][g] = 0.0f;
         // result i of a step joins its accumulators
         auto join_in = [&](int i) {
-            v4f& c = acc[i >> 2][i & 3];
+            const v4f t = tmp[i & 3];
+            v4f c = acc[i >> 2][i & 3];
             const float x = f[(i >> 2) & 1][GATED ? (i & 3) >> 1 : 0];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(tmp[i & 3][r], x, c[r]);
+            c = (v4f){__builtin_fmaf(t[0], x, c[0]), __builtin_fmaf(t[1], x, c[1]), __builtin_fmaf(t[2], x, c[2]),
+                      __builtin_fmaf(t[3], x, c[3])};
             asm volatile("" : "+v"(c));   // here, not behind the next branch
+            acc[i >> 2][i & 3] = c;
         };
 #pragma clang loop unroll(disable)
         for (int s = 0; s < nsteps; ++s) {
             const int nx = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
             const int snx = ssl == SLOTS * SSLOT ? 0 : ssl + SSLOT, spv = ssl == 0 ? SLOTS * SSLOT : ssl - SSLOT;
-            v8h hb[HALF ? NT : 1][4], ha[4];
+            v16i hb[HALF ? NT : 1], ha;
             if constexpr (HALF) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) fp8_to_f16(fb[n], hb[n]);
+                for (int n = 0; n < NT; ++n) hb[n] = fp8_to_f16(fb[n]);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -644,7 +654,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
                     asm volatile("" ::: "memory");
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if constexpr (HALF) fp8_to_f16(fa[m & 1], ha);
+                if constexpr (HALF) ha = fp8_to_f16(fa[m & 1]);
 #pragma unroll
                 for (int g = 0; g < G; ++g) f[m & 1][g] = mul_rn(sa[m & 1], sb[g]);
 #pragma unroll
@@ -687,7 +697,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             else fp8_put_gated<BM, false>(a, acc, cur.m0, cur.rows, cur.tn, wm, wn, j, q, cur.e, (uint32_t*)(smem + TOP));
         } else {
             const int64_t n0 = (int64_t)cur.tn * 256;
-            const int c0 = wn * 64 + 16 * q;
+            const int c0 = wn * 64 + 8 * q;
             if constexpr (HALF) fp8_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else if (a.out_dtype == BF16) fp8_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else fp8_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
