@@ -1668,7 +1668,7 @@ def w4a4_route_experts_scored(logits: torch.Tensor, top_k: int, scores: str = "s
 
 
 def w8a8_experts_fp8_workspace_size(T: int, K: int, F: int, E: int, top_k: int, dtype: torch.dtype) -> int:
-    """Bytes for w8a8_experts_fp8; dtype is that of the experts' rows (rows_dtype, else x's)."""
+    """Bytes for w8a8_experts_fp8; dtype is that of the experts' rows (rows_dtype, else float32)."""
     return int(lib().w8a8_experts_fp8_workspace_size(T, K, F, E, top_k, _DT[dtype]))
 
 
@@ -1682,7 +1682,7 @@ def w8a8_experts_fp8(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_code
     route (as w4a4_route_experts_scored), quantize (rotated by h first if given), gated
     product with w13 (E, 2 F, K; F gates then F ups, F % 128 == 0), product with w2 (E,
     K, F), weighted sum per token.  The experts' rows wait for the sum in rows_dtype:
-    x's (a 16-bit layer then rounds twice), or float32."""
+    float32, or x's (half the bytes, but a 16-bit layer then rounds twice)."""
     lead = _need(x, "x", contiguous=False).shape[:-1]
     x2 = _as_2d(x)
     T, K = x2.shape
@@ -1702,7 +1702,7 @@ def w8a8_experts_fp8(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_code
     how = _scoring(E, top_k, scores, bias, groups, top_groups, group_best, renormalize, scale)
     if out is not None:
         _need(out, "out", (T, K), (x2.dtype,))
-    rows_dtype = rows_dtype or x2.dtype
+    rows_dtype = rows_dtype or torch.float32
     if rows_dtype not in (x2.dtype, torch.float32):
         raise ValueError(f"rows_dtype {rows_dtype} is not {x2.dtype} or float32")
     _same_device(x2, sign_in=si, sign_out=so, logits=logits, bias=bias, w13_codes=w13_codes, w13_scales=w13_scales,

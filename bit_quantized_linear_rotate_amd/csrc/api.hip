@@ -363,6 +363,8 @@ int fp8_grouped_validate(const Fp8GemmArgs& a)
     if (a.R > 0 && !a.offsets) return fail(W4A4_INVALID, "offsets is NULL");
     if (!a.rows && a.M != a.R)
         return fail(W4A4_INVALID, "%lld rows of codes for %lld sorted rows and no row index", (long long)a.M, (long long)a.R);
+    if (a.N * (a.out_codes ? 1 : (int64_t)dsize(a.out_dtype)) >= kFp8MaxRowBytes)
+        return fail(W4A4_UNSUPPORTED, "N=%lld: grouped outputs of 2^23 bytes a row and more", (long long)a.N);
     if (a.rows && a.M * a.K > (int64_t)1 << 31)
         return fail(W4A4_UNSUPPORTED, "codes of more than 2^31 bytes behind a row index");
     return W4A4_OK;
@@ -1441,7 +1443,8 @@ int w8a8_dequantize_weights_fp8(const uint8_t* codes, const float* scales, int64
 int w8a8_gemm_fp8(const uint8_t* codes, const float* scales, int64_t M, int64_t K, const uint8_t* w_codes,
                   const float* w_scales, int64_t N, const void* bias, int bias_dtype, void* out, int out_dtype, void* stream)
 {
-    const Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    a.half = out_dtype == W4A4_F32;
     int rc = fp8_gemm_validate(a);
     if (rc || M == 0 || N == 0) return rc;
     rc = device_check();
@@ -1483,7 +1486,8 @@ int w8a8_linear_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t st
         return fail(W4A4_INVALID, "workspace of %zu bytes, need %zu", workspace_bytes, w8a8_linear_fp8_workspace_size(M, K));
     uint8_t* codes = (uint8_t*)workspace;
     float* scales = (float*)(codes + align256(fp8_codes_bytes(M, K)));
-    const Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, x_dtype, out, out_dtype};
+    Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, x_dtype, out, out_dtype};
+    a.half = out_dtype == W4A4_F32;
     rc = fp8_gemm_validate(a);
     if (rc) return rc;
     rc = device_check();
@@ -1501,6 +1505,7 @@ int w8a8_grouped_gemm_fp8(const uint8_t* codes, const float* scales, int64_t M, 
                           int64_t R, const void* bias, int bias_dtype, void* out, int out_dtype, void* stream)
 {
     Fp8GemmArgs a{codes, scales, M, K, N, w_codes, w_scales, bias, bias_dtype, out, out_dtype};
+    a.half = out_dtype == W4A4_F32;
     a.E = E;
     a.R = R;
     a.offsets = offsets;
@@ -1598,6 +1603,7 @@ int w8a8_experts_fp8(const void* x, int x_dtype, int64_t T, int64_t K, int64_t s
     rc = fp8_gated_validate(g1);
     if (rc) return rc;
     Fp8GemmArgs g2{g1.out_codes, g1.out_scales, R, F, K, w2_codes, w2_scales, nullptr, 0, ws + at.y, rows_dtype};
+    g2.half = x_dtype == W4A4_F32;
     g2.E = E;
     g2.R = R;
     g2.offsets = offsets;

@@ -46,6 +46,7 @@ struct Fp8GemmArgs {
     int bias_dtype;
     void* out;                     // (M, N), or (R, N)
     int out_dtype;
+    bool half = false;             // products on the fp16 matrix cores: sums as exact as fp32 outputs
     // grouped by expert (E > 0): sorted row i of [offsets[e], offsets[e + 1])
     // is row rows[i] of a (row i where rows is null)
     int E = 0;
@@ -57,6 +58,7 @@ struct Fp8GemmArgs {
     uint8_t* out_codes = nullptr;       // (R, N/2)
     float* out_scales = nullptr;        // (N/256, R)
 };
+constexpr int64_t kFp8MaxRowBytes = (int64_t)1 << 23;   // of outputs, in the tile kernel
 // the kernel a call takes (host-only)
 enum { kFp8Skinny = 0, kFp8Tile64 = 1, kFp8Tile128 = 2, kFp8Tile256 = 3 };
 int fp8_gemm_path(const Fp8GemmArgs& a);

@@ -15,8 +15,8 @@
 // beside one of 1 is lost inside such a group, kept outside it), and the groups in
 // fp32.  For random rows that is 1.5e-5 of a sum, a hundredth of the rounding to 16
 // bits and less of that to codes; where the output is fp32 it would be the largest
-// error of all, so those products convert the codes (exactly) to fp16, whose matrix
-// core (16x16x32, half the rate) is 1e-8 off.
+// error of all, so those products (Fp8GemmArgs::half) convert the codes (exactly) to
+// fp16, whose matrix core (16x16x32, half the rate) is 1e-8 off.
 #include "common.hpp"
 #include "fp8.hpp"
 #include "fp8_codes.hpp"
@@ -79,66 +79,42 @@ __device__ __forceinline__ void fp8_zero_rows(const Fp8GemmArgs& a, int64_t part
 }
 
 // ---- the skinny kernel -------------------------------------------------------
-// Few rows: the weights are the cost, read once, straight into registers.  A
-// workgroup of eight waves takes 16 MT rows; KW of its waves share the K steps of
-// one group of 16 NT columns, 8 / KW groups lie side by side (gated: a group is 16
-// gates and their 16 ups, KW = 1, and the eight groups are one block of 128
-// results).  Partial sums meet in LDS and are added in wave order.
+// Few rows, dense: the weights are the cost, read once, straight into registers.  A
+// workgroup of eight waves takes 16 MT rows; KW of its waves share the K steps of one
+// group of 16 NT columns, 8 / KW groups lie side by side.  Partial sums meet in LDS
+// and are added in wave order.  The matrix cores wait for memory here, so all types
+// take the fp16 products.
+// Bound by the weights' bytes and, up to a few megabytes of them, by latency: 3840 x
+// 3840 weights with one row 5.0 us, 10240 x 10240 (105 MB) 21 us = 5 TB/s, with 32 rows
+// 44 us, each column group reading the rows again.
+// (Grouped by expert, 64-row tiles are as fast or faster from one row an expert on: 32
+// experts of 3840 x 2560, a mean of 1, 4, 16 rows: 24, 62, 68 us where this kernel's
+// grouped form took 24, 62, 89, and gated 28, 63, 67 for 38, 77, 91.)
 constexpr int kSkinnyWaves = 8;
-template <int MT, int NT, int KW, bool GROUPED, bool GATED, bool HALF>
-__global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
+template <int MT, int NT, int KW> __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
 {
-    static_assert(!GATED || (NT == 2 && KW == 1), "a block of results per workgroup");
-    constexpr int W = kSkinnyWaves, CG = W / KW;
-    constexpr int COLS = GATED ? 16 : 16 * NT;   // results of a column group
+    constexpr int W = kSkinnyWaves, CG = W / KW, COLS = 16 * NT;
     __shared__ float part[W][MT][NT][16][17];    // [wave][row tile][column tile][row][column]
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int kw = wave % KW, cg = wave / KW;
     const int j = lane & 15, q = lane >> 4;
-    const int64_t K = a.K, N = a.N, F = N >> 1;
-    const int64_t n = GATED ? F : N;             // results of a row
+    const int64_t K = a.K, N = a.N;
     const int nsteps = (int)fp8_blocks(K);
-    int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-    int rows, e = 0;
-    if constexpr (GROUPED) {
-        MxRows r;
-        const int64_t total = mx_find<16 * MT, true>(a, blockIdx.y, r);
-        if (r.e < 0) {
-            fp8_zero_rows(a, (int64_t)(blockIdx.y - total) * gridDim.x + blockIdx.x, (int64_t)(gridDim.y - total) * gridDim.x);
-            return;
-        }
-        const int m = (int)(blockIdx.y - r.before);
-        e = r.e;
-        m0 = r.m0 + (int64_t)m * (16 * MT);
-        rows = min(r.rows - m * 16 * MT, 16 * MT);
-    } else {
-        rows = (int)min(a.M - m0, (int64_t)(16 * MT));
-    }
-    const uint8_t* wb = a.b + (int64_t)e * N * K;
-    const float* wsb = a.sb + (int64_t)e * fp8_blocks(N) * nsteps;
-    const int64_t first = ((int64_t)blockIdx.x * CG + cg) * COLS;   // the group's first result
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int rows = (int)min(a.M - m0, (int64_t)(16 * MT));
+    const int64_t first = ((int64_t)blockIdx.x * CG + cg) * COLS;   // the group's first column
     // this lane's weight columns and rows (clamped: what they give is not stored)
     int64_t col[NT], src[MT];
     const float* ws[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int64_t c = first + (GATED ? 0 : nt * 16);
-        const int64_t up = GATED ? nt * F : 0;
-        col[nt] = min(c + j, n - 1) + up;
-        ws[nt] = wsb + (min(c, n - 1) + up) / kFp8Block * nsteps;
+        const int64_t c = first + nt * 16;
+        col[nt] = min(c + j, N - 1);
+        ws[nt] = a.sb + min(c, N - 1) / kFp8Block * nsteps;
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int i = 16 * mt + j;
-        int64_t s = m0 + (i < rows ? i : rows - 1);
-        bool ok = true;
-        if (GROUPED && a.rows) {
-            s = a.rows[s];
-            ok = s >= 0 && s < a.M;
-        }
-        src[mt] = ok ? s : -1;
-    }
+    for (int mt = 0; mt < MT; ++mt) src[mt] = m0 + min(16 * mt + j, rows - 1);
     v4f acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -155,18 +131,17 @@ __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
             const int64_t k = (int64_t)s * kFp8Block + 32 * q;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const uint8_t* p = wb + col[nt] * K + k;
+                const uint8_t* p = a.b + col[nt] * K + k;
                 fb[u][nt][0] = in && k < K ? *(const v4i*)p : (v4i){0, 0, 0, 0};
                 fb[u][nt][1] = in && k + 16 < K ? *(const v4i*)(p + 16) : (v4i){0, 0, 0, 0};
                 sw[u][nt] = in ? ws[nt][s] : 0.0f;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const bool ok = in && src[mt] >= 0;
                 const uint8_t* p = a.a + src[mt] * K + k;
-                fa[u][mt][0] = ok && k < K ? *(const v4i*)p : (v4i){0, 0, 0, 0};
-                fa[u][mt][1] = ok && k + 16 < K ? *(const v4i*)(p + 16) : (v4i){0, 0, 0, 0};
-                sa[u][mt] = ok ? a.sa[(int64_t)s * a.M + src[mt]] : 0.0f;
+                fa[u][mt][0] = in && k < K ? *(const v4i*)p : (v4i){0, 0, 0, 0};
+                fa[u][mt][1] = in && k + 16 < K ? *(const v4i*)(p + 16) : (v4i){0, 0, 0, 0};
+                sa[u][mt] = in ? a.sa[(int64_t)s * a.M + src[mt]] : 0.0f;
             }
         }
 #pragma unroll
@@ -175,12 +150,7 @@ __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    v4f p;
-                    if constexpr (HALF) {
-                        p = f16_mfma(fp8_to_f16(join(fb[u][nt][0], fb[u][nt][1])), fp8_to_f16(join(fa[u][mt][0], fa[u][mt][1])));
-                    } else {
-                        p = fp8_mfma(join(fb[u][nt][0], fb[u][nt][1]), join(fa[u][mt][0], fa[u][mt][1]));
-                    }
+                    const v4f p = f16_mfma(fp8_to_f16(join(fb[u][nt][0], fb[u][nt][1])), fp8_to_f16(join(fa[u][mt][0], fa[u][mt][1])));
                     const float f = mul_rn(sa[u][mt], sw[u][nt]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc[mt][nt][r] = __builtin_fmaf(p[r], f, acc[mt][nt][r]);
@@ -195,46 +165,15 @@ __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
             for (int r = 0; r < 4; ++r) part[wave][mt][nt][j][4 * q + r] = acc[mt][nt][r];
     __syncthreads();
     const int waves = nsteps < KW ? nsteps : KW;   // those that had a step
-    auto sum = [&](int g, int mt, int nt, int row, int c) {
-        float v = part[g * KW][mt][nt][row][c];
-        for (int w = 1; w < waves; ++w) v = add_rn(v, part[g * KW + w][mt][nt][row][c]);
-        return v;
-    };
-    if constexpr (GATED) {
-        // half a wave takes the 128 results of a row, four a lane
-        const int l = tid & 31;
-        const int64_t f0 = (int64_t)blockIdx.x * kFp8Block, f = f0 + 4 * l;
-        for (int row = tid >> 5; row < 16 * MT; row += 16) {
-            if (row >= rows) continue;   // (whole half waves)
-            const int mt = row >> 4;
-            float v[4];
-            uint32_t m = 0;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float g = sum(l >> 2, mt, 0, row & 15, 4 * (l & 3) + r), u = sum(l >> 2, mt, 1, row & 15, 4 * (l & 3) + r);
-                if (a.bias) {
-                    g = add_rn(g, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + f + r));
-                    u = add_rn(u, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + F + f + r));
-                }
-                v[r] = mx_gated(g, u);
-                m = max(m, __float_as_uint(v[r]) & 0x7fffffffu);
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-            const Fp8Block b = fp8_block(m);
-            *(uint32_t*)(a.out_codes + (m0 + row) * F + f) = fp8_codes4(b, v[0], v[1], v[2], v[3]);
-            if (l == 0) a.out_scales[(int64_t)blockIdx.x * a.R + m0 + row] = b.scale;
-        }
-    } else {
-        constexpr int WG = CG * COLS;
-        for (int i = tid; i < 16 * MT * WG; i += 512) {
-            const int row = i / WG, c = i % WG, g = c / COLS, nt = (c % COLS) >> 4;
-            const int64_t nn = (int64_t)blockIdx.x * WG + c;
-            if (nn < N && row < rows) {
-                float v = sum(g, row >> 4, nt, row & 15, c & 15);
-                if (a.bias) v = add_rn(v, load_any_f32(a.bias_dtype, a.bias, (int64_t)e * N + nn));
-                store_any(a.out_dtype, a.out, (m0 + row) * N + nn, v);
-            }
+    constexpr int WG = CG * COLS;
+    for (int i = tid; i < 16 * MT * WG; i += 512) {
+        const int row = i / WG, c = i % WG, g = c / COLS, nt = (c % COLS) >> 4, mt = row >> 4;
+        const int64_t nn = (int64_t)blockIdx.x * WG + c;
+        if (nn < N && row < rows) {
+            float v = part[g * KW][mt][nt][row & 15][c & 15];
+            for (int w = 1; w < waves; ++w) v = add_rn(v, part[g * KW + w][mt][nt][row & 15][c & 15]);
+            if (a.bias) v = add_rn(v, load_any_f32(a.bias_dtype, a.bias, nn));
+            store_any(a.out_dtype, a.out, (m0 + row) * N + nn, v);
         }
     }
 }
@@ -698,7 +637,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
         } else {
             const int64_t n0 = (int64_t)cur.tn * 256;
             const int c0 = wn * 64 + 8 * q;
-            if constexpr (HALF) fp8_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
+            if (HALF || a.out_dtype == F32) fp8_epilogue<F32, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else if (a.out_dtype == BF16) fp8_epilogue<BF16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
             else fp8_epilogue<F16, MT>(a, acc, cur.m0, row0, cur.rows, n0, c0, cur.e);
         }
@@ -710,32 +649,29 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     }
 }
 
-int skinny_rows(const Fp8GemmArgs& a)
+int skinny_rows(const Fp8GemmArgs& a) { return a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64; }
+
+// 32 columns a group once 16 would make more workgroups than the CUs hold: the rows
+// are read half as often.
+int skinny_cols(const Fp8GemmArgs& a)
 {
-    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return (a.N + 15) / 16 * ((a.M + skinny_rows(a) - 1) / skinny_rows(a)) <= 512 ? 16 : 32;
 }
 
-template <int MT, int NT, int KW, bool GATED, bool HALF = false> hipError_t launch_skinny_w(const Fp8GemmArgs& a, hipStream_t st)
+template <int MT, int NT, int KW> hipError_t launch_skinny_w(const Fp8GemmArgs& a, hipStream_t st)
 {
-    constexpr int COLS = (GATED ? 16 : 16 * NT) * (kSkinnyWaves / KW);
-    const int64_t n = GATED ? a.N / 2 : a.N;
-    const unsigned tn = (unsigned)((n + COLS - 1) / COLS);
-    if (a.E) {
-        const unsigned tm = (unsigned)(a.R / (16 * MT) + (a.E < a.R ? a.E : a.R) + 1);
-        hipLaunchKernelGGL((fp8_skinny_kernel<MT, NT, KW, true, GATED, HALF>), dim3(tn, tm), dim3(512), 0, st, a);
-    } else if constexpr (!GATED) {
-        hipLaunchKernelGGL((fp8_skinny_kernel<MT, NT, KW, false, false, HALF>), dim3(tn, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
-                           dim3(512), 0, st, a);
-    }
+    constexpr int COLS = 16 * NT * (kSkinnyWaves / KW);
+    hipLaunchKernelGGL((fp8_skinny_kernel<MT, NT, KW>), dim3((unsigned)((a.N + COLS - 1) / COLS), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
+                       dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
 template <int MT> hipError_t launch_skinny(const Fp8GemmArgs& a, hipStream_t st)
 {
-    if (a.out_codes) return launch_skinny_w<MT, 2, 1, true>(a, st);
-    if (a.out_dtype == F32) return launch_skinny_w<MT, 1, 8, false, true>(a, st);
-    return launch_skinny_w<MT, 1, 8, false>(a, st);
+    // half the waves per column group where K has few steps for eight of them
+    const bool deep = a.K > 1024;
+    if (skinny_cols(a) == 16) return deep ? launch_skinny_w<MT, 1, 8>(a, st) : launch_skinny_w<MT, 1, 4>(a, st);
+    return deep ? launch_skinny_w<MT, 2, 8>(a, st) : launch_skinny_w<MT, 2, 4>(a, st);
 }
 
 // One workgroup per CU (LDS holds one), which takes tiles in turn.
@@ -757,26 +693,57 @@ template <int BM, bool HALF> hipError_t launch_tile(const Fp8GemmArgs& a, hipStr
     return hipGetLastError();
 }
 
+// Estimated microseconds of each kernel.  Tiles: the 256 workgroups take them in
+// rounds; a step of a 64, 128, 256 row tile measured 0.63, 0.95, 1.63 us with all CUs
+// busy, a tile's beginning and end 4.3, 7.8, 11.5 (1024, 2048, 4096 rows of 4096
+// outputs at K = 1280 and 3840: 13.2 and 25.6, 18.9 and 39.0, 28.4 and 63.9 us); with
+// fp16 products 1.74.
+// Skinny: the weights, and for each column group the rows again, at 5 TB/s (10240 x
+// 10240 weights with 1, 16, 32, 64 rows: 21, 30, 44, 65 us; with 64-row tiles 46).
+// The groups' sizes are on the device: all are taken to have the mean, and to fill
+// half of their last tile (ragged groups of 32 experts of 3840 x 2560 with a mean of
+// 128, 256, 512, 1024 rows: 115, 158, 276, 500 us with 64 rows a tile, 89, 158, 233, 404
+// with 128, 119, 134, 228, 361 with 256).
+double tile_us(const Fp8GemmArgs& a, int bm, double step, double ends)
+{
+    const double tn = a.out_codes ? (double)(a.N / 2 / kFp8Block) : (double)((a.N + 255) / 256);
+    double tm = (double)((a.M + bm - 1) / bm);
+    if (a.E) {
+        const double groups = (double)(a.E < a.R ? a.E : a.R);
+        tm = (double)a.R / bm + 0.5 * groups;
+    }
+    const double rounds = tm * tn < 1 ? 1 : (double)(int64_t)((tm * tn + 255) / 256);
+    return 2.5 + rounds * ((double)fp8_blocks(a.K) * step + ends);
+}
+
+double skinny_us(const Fp8GemmArgs& a)
+{
+    const double weights = (double)a.N * (double)a.K * 1e-6;   // MB
+    return 2.5 + (weights * (double)((a.M + skinny_rows(a) - 1) / skinny_rows(a)) + weights * (double)a.M / skinny_cols(a)) / 5.0;
+}
+
 }  // namespace
 
 int fp8_gemm_path(const Fp8GemmArgs& a)
 {
-    const int64_t rows = a.E ? (a.R + a.E - 1) / a.E : a.M;
-    const bool half = !a.out_codes && a.out_dtype == F32;
+    const double t[4] = {skinny_us(a), tile_us(a, 64, 0.63, 4.3), tile_us(a, 128, a.half ? 1.74 : 0.95, 7.8), tile_us(a, 256, 1.63, 11.5)};
+    int best = a.half ? kFp8Tile128 : kFp8Tile64;
+    if (!a.half)
+        for (int i = kFp8Tile128; i <= kFp8Tile256; ++i)
+            if (t[i] < t[best]) best = i;
+    if (a.E) return best;
     // A tile's outputs are addressed with 31 bits: rows of 8 MB and more are the
     // skinny kernel's.
-    if (a.N * (a.out_codes ? 1 : a.out_dtype == F32 ? 4 : 2) >= (int64_t)1 << 23) return kFp8Skinny;
-    if (rows <= 64) return kFp8Skinny;
-    if (half) return kFp8Tile128;
-    return rows <= 128 ? kFp8Tile64 : rows <= 512 ? kFp8Tile128 : kFp8Tile256;
+    if (a.N * (a.out_dtype == F32 ? 4 : 2) >= kFp8MaxRowBytes) return kFp8Skinny;
+    // (past 128 rows the weights would be read three times and more)
+    return a.M <= 128 && t[kFp8Skinny] < t[best] ? kFp8Skinny : best;
 }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t st)
 {
-    const bool half = !a.out_codes && a.out_dtype == F32;
     switch (fp8_gemm_path(a)) {
     case kFp8Tile256: return launch_tile<256, false>(a, st);
-    case kFp8Tile128: return half ? launch_tile<128, true>(a, st) : launch_tile<128, false>(a, st);
+    case kFp8Tile128: return a.half ? launch_tile<128, true>(a, st) : launch_tile<128, false>(a, st);
     case kFp8Tile64: return launch_tile<64, false>(a, st);
     }
     const int rows = skinny_rows(a);

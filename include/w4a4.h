@@ -454,8 +454,8 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
  *   infinity gets the scale NaN and codes 0.  K is a multiple of 16, at most 2^22; at
  *   most 2^28 rows.  The products refuse (W4A4_UNSUPPORTED) activations of more than
  *   2^31 bytes of scales, codes of more than 2^31 bytes behind a row index (so the
- *   expert layer's x), more than 16384 experts, and outputs of R x N (M x N) with
- *   (R / 64 + E + 1) (N / 128 + 1) >= 2^22.
+ *   expert layer's x), more than 16384 experts, grouped outputs of 2^23 bytes a row
+ *   and more, and outputs of R x N (M x N) with (R / 64 + E + 1) (N / 128 + 1) >= 2^22.
  *
  * w8a8_quantize_fp8: rows of x (any strides; 16-byte aligned contiguous rows take
  *   wide loads), rotated first if g > 0, as for w4a4_quantize_mx4.
@@ -466,6 +466,9 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
  *   times scale in fp32, rounded once more to 16 bits), 16-byte aligned.
  * w8a8_gemm_fp8: out[m][n] = O(sum_b sa[b][m] sw[n/128][b] (sum_{k in b} a[m][k]
  *   w[n][k]) + bias[n]), fp32 sums, the inner ones on the matrix cores.
+ *   The fp8 matrix core adds eight neighbouring products to 2^-13 of the largest
+ *   (1.5e-5 of a sum of random rows); fp32 outputs take the fp16 matrix core, half as
+ *   fast, with sums as exact as fp32.
  * w8a8_linear_fp8: quantiser and product back to back; bias in x_dtype; a workspace
  *   of w8a8_linear_fp8_workspace_size(M, K) bytes, 16-byte aligned.
  * w8a8_grouped_gemm_fp8: sorted rows, offsets and row index as for
@@ -490,8 +493,8 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
  *   groups <= 64 divides E, top_k <= (E / groups) * top_groups.
  * w8a8_experts_fp8: w4a4_route_experts_scored, quantise, gated product (w13: (E, 2 F,
  *   K), gates first, F a multiple of 128), product (w2: (E, K, F)), combine; the
- *   experts' rows are kept in rows_dtype, x_dtype (a 16-bit layer then rounds twice)
- *   or W4A4_F32.  No biases of the products; T * top_k < 2^28.  Workspace of
+ *   experts' rows are kept in rows_dtype, W4A4_F32 or x_dtype (half the bytes; a
+ *   16-bit layer then rounds twice).  No biases of the products; T * top_k < 2^28.  Workspace of
  *   w8a8_experts_fp8_workspace_size(.., rows_dtype) bytes, 16-byte aligned.
  */
 int w8a8_quantize_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,

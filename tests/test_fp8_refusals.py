@@ -129,7 +129,7 @@ def test_abi_refuses():
     grp = lambda **o: c("w8a8_grouped_gemm_fp8", *{**dict(codes=P, scales=P, M=4, K=64, w=P, ws=P, E=2, N=16, off=P, rows=P,  # noqa: E731
                                                            R=8, bias=None, bdt=0, out=P, odt=2, st=None), **o}.values())
     assert grp(E=0) == I and grp(off=None) == I and grp(R=-1) == I and grp(rows=None) == I and grp(R=1 << 31) == U
-    assert grp(E=20000) == U and grp(M=1 << 22, K=1024) == U
+    assert grp(E=20000) == U and grp(M=1 << 22, K=1024) == U and grp(N=1 << 22) == U and grp(N=1 << 21, odt=0) == U
     gat = lambda **o: c("w8a8_grouped_gated_fp8", *{**dict(codes=P, scales=P, M=4, K=64, w=P, ws=P, E=2, N=256, off=P, rows=P,  # noqa: E731
                                                             R=8, bias=None, bdt=0, oc=P, os=P, st=None), **o}.values())
     assert gat(N=128) == I and gat(oc=None) == I and gat(os=None) == I and gat(oc=P + 8) == U

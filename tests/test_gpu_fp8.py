@@ -181,7 +181,11 @@ def test_ties_go_to_the_even_code():
 # rows, K, N: every kernel, widths that no tile divides, K that ends inside a block
 GEMMS = [(1, 16, 16), (1, 3840, 48), (5, 272, 130), (16, 400, 257), (17, 128, 64), (40, 1040, 300), (64, 512, 1000),
          (100, 640, 256), (129, 272, 513), (200, 1296, 2304), (333, 384, 1001), (700, 528, 2305), (1500, 272, 3841),
-         (2049, 1040, 2560), (4100, 272, 1280)]
+         (2049, 1040, 2560), (4100, 272, 1280), (3000, 400, 4099), (5000, 144, 2305)]
+
+
+def test_sizes_reach_every_kernel():
+    assert {w4.w8a8_gemm_fp8_plan(M, K, N) for M, K, N in GEMMS} == {"skinny", "tile64", "tile128", "tile256"}
 
 
 @pytest.mark.parametrize("M,K,N", GEMMS)
