@@ -1465,6 +1465,7 @@ int w8a8_gemm_fp8_plan(int64_t rows, int64_t K, int64_t N, int32_t E, int32_t ga
     a.E = E;
     a.R = rows;
     if (gated) a.out_codes = (uint8_t*)16;
+    a.half = gated != 0;
     *kernel = rows == 0 || N == 0 ? -1 : fp8_gemm_path(a);
     return W4A4_OK;
 }
@@ -1529,6 +1530,7 @@ int w8a8_grouped_gated_fp8(const uint8_t* codes, const float* scales, int64_t M,
     a.rows = rows;
     a.out_codes = out_codes;
     a.out_scales = out_scales;
+    a.half = true;
     if (R > 0 && N > 0 && (!out_codes || !out_scales)) return fail(W4A4_INVALID, "out_codes/out_scales is NULL");
     int rc = fp8_gated_validate(a);
     if (rc || R == 0 || N == 0) return rc;
@@ -1600,6 +1602,7 @@ int w8a8_experts_fp8(const void* x, int x_dtype, int64_t T, int64_t K, int64_t s
     g1.rows = rows;
     g1.out_codes = ws + at.act_codes;
     g1.out_scales = (float*)(ws + at.act_scales);
+    g1.half = true;
     rc = fp8_gated_validate(g1);
     if (rc) return rc;
     Fp8GemmArgs g2{g1.out_codes, g1.out_scales, R, F, K, w2_codes, w2_scales, nullptr, 0, ws + at.y, rows_dtype};

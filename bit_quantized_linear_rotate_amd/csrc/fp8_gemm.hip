@@ -14,9 +14,13 @@
 // point, 2^-13 of the largest of them the last place (measured: a product of 2^-14
 // beside one of 1 is lost inside such a group, kept outside it), and the groups in
 // fp32.  For random rows that is 1.5e-5 of a sum, a hundredth of the rounding to 16
-// bits and less of that to codes; where the output is fp32 it would be the largest
-// error of all, so those products (Fp8GemmArgs::half) convert the codes (exactly) to
-// fp16, whose matrix core (16x16x32, half the rate) is 1e-8 off.
+// bits.  Where the output is fp32 it would be the largest
+// error of all, and in a gated product it would move one code in two thousand over a
+// border (an error of its own of 1e-3 where the codes are the result).  Those products
+// (Fp8GemmArgs::half) convert the codes (exactly) to fp16, whose matrix core (16x16x32,
+// half the rate) is 1e-8 off.
+#include <type_traits>
+
 #include "common.hpp"
 #include "fp8.hpp"
 #include "fp8_codes.hpp"
@@ -356,7 +360,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int j = lane & 15, q = lane >> 4;
-    const int wm = wave & 1, wn = wave >> 1;
+    const int wm = wave >> 2, wn = wave & 3;   // (a SIMD's two waves: one of each half of the rows)
     const int64_t K = a.K, N = a.N;
     const int nsteps = (int)fp8_blocks(K);
     const int chunks = (int)(K >> 4);
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int nt = (wave & 1) * 2 + (i >> 1), idx = (i & 1) * 8 + l8;
-            const int c = (GATED ? wn * 32 : wn * 64 + 32 * (nt >> 1)) + 8 * (idx >> 2) + 4 * (nt & 1) + (idx & 3);
+            const int c = (GATED ? (wave >> 1) * 32 : (wave >> 1) * 64 + 32 * (nt >> 1)) + 8 * (idx >> 2) + 4 * (nt & 1) + (idx & 3);
             bvo[i] = col0 + c < ncols ? (uint32_t)(c * (uint32_t)K + (ch ^ ((i & 1) * 4)) * 16) : kOut;
         }
         const int64_t brow = (int64_t)t.e * N + col0 + (GATED && (wave & 1) ? F : 0);
@@ -564,69 +568,83 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
             asm volatile("" : "+v"(c));   // here, not behind the next branch
             acc[i >> 2][i & 3] = c;
         };
+        // all steps of a tile; LIVE: with the arithmetic
+        auto steps = [&](auto live) {
+            constexpr bool LIVE = decltype(live)::value;
 #pragma clang loop unroll(disable)
-        for (int s = 0; s < nsteps; ++s) {
-            const int nx = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
-            const int snx = ssl == SLOTS * SSLOT ? 0 : ssl + SSLOT, spv = ssl == 0 ? SLOTS * SSLOT : ssl - SSLOT;
-            v16i hb[HALF ? NT : 1], ha;
-            if constexpr (HALF) {
+            for (int s = 0; s < nsteps; ++s) {
+                const int nx = sl == (SLOTS - 1) * SLOT ? 0 : sl + SLOT;
+                const int snx = ssl == SLOTS * SSLOT ? 0 : ssl + SSLOT, spv = ssl == 0 ? SLOTS * SSLOT : ssl - SSLOT;
+                v16i hb[HALF ? NT : 1], ha;
+                if constexpr (HALF && LIVE) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) hb[n] = fp8_to_f16(fb[n]);
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (m % PH == PH - 1) {
-                    // What the next PH row tiles need has landed, and the last are read.  Still in flight may be all groups sent since and, until
-                    // they are those that followed them, the stores of the tile before.
-                    constexpr int kAll = SLOTS * D;
-                    const int k = m / PH;
-                    const int n0 = kAll - (k == 0 ? G0 : AG) - ((k + 1) % NP == 0 ? G0 : AG);
-                    asm volatile("s_waitcnt lgkmcnt(0)\n\t"
-                                 "s_cmp_lt_i32 %0, 1\n\t"
-                                 "s_cbranch_scc1 1f\n\t"
-                                 "s_waitcnt vmcnt(%1)\n\t"
-                                 "s_branch 2f\n"
-                                 "1:\n\t"
-                                 "s_waitcnt vmcnt(%2)\n"
-                                 "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"(n0 + PUTS), "n"(n0)
-                                 : "memory", "scc");
-                    --stores;
-                    __builtin_amdgcn_s_barrier();
-                    asm volatile("" ::: "memory");
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int n = 0; n < NT; ++n) hb[n] = fp8_to_f16(fb[n]);
                 }
-                if constexpr (HALF) ha = fp8_to_f16(fa[m & 1]);
 #pragma unroll
-                for (int g = 0; g < G; ++g) f[m & 1][g] = mul_rn(sa[m & 1], sb[g]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int i = m * NT + n;
-                    if constexpr (HALF) tmp[i & 3] = f16_mfma(hb[n], ha);
-                    else tmp[i & 3] = fp8_mfma(fb[n], fa[m & 1]);
-                    if (m < MT - 1) {
-                        if (n == 0) read_a(sl, ssl, m + 1);
-                    } else {
-                        // (past the last step: of a slot's older contents, unused)
-                        if (n == 0) read_a(nx, snx, 0);
-                        read(fb[n], nx + bo, n * 16 * 128);
-                        if (n == NT - 1) read_sb(snx);
-                    }
+                for (int m = 0; m < MT; ++m) {
                     if (m % PH == PH - 1) {
-                        const int size = m / PH == 0 ? G0 : AG;
+                        // What the next PH row tiles need has landed, and the last are read.  Still in flight may be all groups sent since and, until
+                        // they are those that followed them, the stores of the tile before.
+                        constexpr int kAll = SLOTS * D;
+                        const int k = m / PH;
+                        const int n0 = kAll - (k == 0 ? G0 : AG) - ((k + 1) % NP == 0 ? G0 : AG);
+                        asm volatile("s_waitcnt lgkmcnt(0)\n\t"
+                                     "s_cmp_lt_i32 %0, 1\n\t"
+                                     "s_cbranch_scc1 1f\n\t"
+                                     "s_waitcnt vmcnt(%1)\n\t"
+                                     "s_branch 2f\n"
+                                     "1:\n\t"
+                                     "s_waitcnt vmcnt(%2)\n"
+                                     "2:" ::"s"(__builtin_amdgcn_readfirstlane(stores)), "n"(n0 + PUTS), "n"(n0)
+                                     : "memory", "scc");
+                        --stores;
+                        __builtin_amdgcn_s_barrier();
+                        asm volatile("" ::: "memory");
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if constexpr (HALF && LIVE) ha = fp8_to_f16(fa[m & 1]);
 #pragma unroll
-                        for (int x = n * size / NT; x < (n + 1) * size / NT; ++x) dma(d, sl, spv, m / PH, x);
+                    for (int g = 0; g < G; ++g) f[m & 1][g] = mul_rn(sa[m & 1], sb[g]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int i = m * NT + n;
+                        if constexpr (!LIVE) (void)0;
+                        else if constexpr (HALF) tmp[i & 3] = f16_mfma(hb[n], ha);
+                        else tmp[i & 3] = fp8_mfma(fb[n], fa[m & 1]);
+                        if (m < MT - 1) {
+                            if (n == 0) read_a(sl, ssl, m + 1);
+                        } else {
+                            // (past the last step: of a slot's older contents, unused)
+                            if (n == 0) read_a(nx, snx, 0);
+                            read(fb[n], nx + bo, n * 16 * 128);
+                            if (n == NT - 1) read_sb(snx);
+                        }
+                        if (m % PH == PH - 1) {
+                            const int size = m / PH == 0 ? G0 : AG;
+#pragma unroll
+                            for (int x = n * size / NT; x < (n + 1) * size / NT; ++x) dma(d, sl, spv, m / PH, x);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                        if constexpr (LIVE) join_in(i >= 3 ? i - 3 : MT * NT - 3 + i);
+                        if (m == 0 && n == 2) {
+                            advance();
+                            dma_of(d, s_dma);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
-                    join_in(i >= 3 ? i - 3 : MT * NT - 3 + i);
-                    if (m == 0 && n == 2) {
-                        advance();
-                        dma_of(d, s_dma);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
+                sl = nx;
+                ssl = snx;
             }
-            sl = nx;
-            ssl = snx;
+        };
+        // Few rows: where a wave's are all past the tile's it only moves data (converting
+        // weights to fp16 costs as much as their products: 32 experts of 3840 x 2560 with
+        // two rows each, gated: 75 -> 66 us).
+        if constexpr (HALF && BM == 64) {
+            if (wm * (BM / 2) < cur.rows) steps(std::true_type{});
+            else steps(std::false_type{});
+        } else {
+            steps(std::true_type{});
         }
 #pragma unroll
         for (int i = MT * NT - 3; i < MT * NT; ++i) join_in(i);
@@ -690,8 +708,8 @@ template <int BM, bool HALF> hipError_t launch_tile(const Fp8GemmArgs& a, hipStr
         hipLaunchKernelGGL((fp8_tile_kernel<BM, false, false, HALF>), dim3(grid), dim3(512), 0, st, a, (int)tm, (int)tn);
     else if (!gated)
         hipLaunchKernelGGL((fp8_tile_kernel<BM, true, false, HALF>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
-    else if constexpr (!HALF)
-        hipLaunchKernelGGL((fp8_tile_kernel<BM, true, true, false>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
+    else if constexpr (HALF)
+        hipLaunchKernelGGL((fp8_tile_kernel<BM, true, true, true>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
     return hipGetLastError();
 }
 
@@ -699,13 +717,14 @@ template <int BM, bool HALF> hipError_t launch_tile(const Fp8GemmArgs& a, hipStr
 // rounds; a step of a 64, 128, 256 row tile measured 0.63, 0.95, 1.63 us with all CUs
 // busy, a tile's beginning and end 4.3, 7.8, 11.5 (1024, 2048, 4096 rows of 4096
 // outputs at K = 1280 and 3840: 13.2 and 25.6, 18.9 and 39.0, 28.4 and 63.9 us); with
-// fp16 products 1.74.
+// fp16 products a step of 64, 128 rows 1.15, 1.74 (256 rows would not fit the registers).
 // Skinny: the weights, and for each column group the rows again, at 5 TB/s (10240 x
 // 10240 weights with 1, 16, 32, 64 rows: 21, 30, 44, 65 us; with 64-row tiles 46).
 // The groups' sizes are on the device: all are taken to have the mean, and to fill
 // half of their last tile (ragged groups of 32 experts of 3840 x 2560 with a mean of
 // 128, 256, 512, 1024 rows: 115, 158, 276, 500 us with 64 rows a tile, 89, 158, 233, 404
-// with 128, 119, 134, 228, 361 with 256).
+// with 128, 119, 134, 228, 361 with 256; gated, fp16 products: 145, 213, 384, 722 and 113,
+// 217, 323, 598; with a mean of 64 rows 78 and 111).
 double tile_us(const Fp8GemmArgs& a, int bm, double step, double ends)
 {
     const double tn = a.out_codes ? (double)(a.N / 2 / kFp8Block) : (double)((a.N + 255) / 256);
@@ -728,11 +747,10 @@ double skinny_us(const Fp8GemmArgs& a)
 
 int fp8_gemm_path(const Fp8GemmArgs& a)
 {
-    const double t[4] = {skinny_us(a), tile_us(a, 64, 0.63, 4.3), tile_us(a, 128, a.half ? 1.74 : 0.95, 7.8), tile_us(a, 256, 1.63, 11.5)};
-    int best = a.half ? kFp8Tile128 : kFp8Tile64;
-    if (!a.half)
-        for (int i = kFp8Tile128; i <= kFp8Tile256; ++i)
-            if (t[i] < t[best]) best = i;
+    const double t[4] = {skinny_us(a), tile_us(a, 64, a.half ? 1.15 : 0.63, 4.3), tile_us(a, 128, a.half ? 1.74 : 0.95, 7.8), tile_us(a, 256, 1.63, 11.5)};
+    int best = kFp8Tile64;
+    for (int i = kFp8Tile128; i <= (a.half ? kFp8Tile128 : kFp8Tile256); ++i)
+        if (t[i] < t[best]) best = i;
     if (a.E) return best;
     // A tile's outputs are addressed with 31 bits: rows of 8 MB and more are the
     // skinny kernel's.
@@ -746,7 +764,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t st)
     switch (fp8_gemm_path(a)) {
     case kFp8Tile256: return launch_tile<256, false>(a, st);
     case kFp8Tile128: return a.half ? launch_tile<128, true>(a, st) : launch_tile<128, false>(a, st);
-    case kFp8Tile64: return launch_tile<64, false>(a, st);
+    case kFp8Tile64: return a.half ? launch_tile<64, true>(a, st) : launch_tile<64, false>(a, st);
     }
     const int rows = skinny_rows(a);
     return rows == 16 ? launch_skinny<1>(a, st) : rows == 32 ? launch_skinny<2>(a, st) : launch_skinny<4>(a, st);
