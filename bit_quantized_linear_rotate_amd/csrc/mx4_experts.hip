@@ -213,6 +213,12 @@ template <int DT, int L, int NV, bool ONE> __global__ __launch_bounds__(1024) vo
 // wave chooses it again in double precision.  Without a bias the scores' order is the
 // logits', and (unless groups are ranked by sums) nothing is in doubt.  The weights
 // are computed in double precision, a choice to a lane.
+// Bounds.  The logits are 8 MB at the most; what counts are the k dependent rounds
+// over lanes, the exponentials, and fetching the code (every variant on sizes is its
+// own kernel, straight through).  Measured: 32 tokens of 128 experts, 8 choices,
+// softmax 8.0 us with the sort (in double precision throughout 11.4); 8192 tokens of
+// 256, 8 choices, 4 of 8 groups by their two largest, sigmoid and bias 31 us (64), and the sort
+// 7.4; of 32 experts, 4 choices, 4 groups 13.8; 16 tokens of those 10.1 with the sort.
 
 // the value of the lane whose index differs in bits D, for the lanes of one token
 template <int L> __device__ __forceinline__ double lanes_max64(double v)

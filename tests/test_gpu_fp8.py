@@ -9,6 +9,11 @@ from tests.gpu_util import need_gpu
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(7)
+
 import bit_quantized_linear_rotate_amd as w4  # noqa: E402
 
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}

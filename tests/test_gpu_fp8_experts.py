@@ -10,6 +10,11 @@ from tests.test_gpu_fp8 import DT, F8, as64, draw_x, raw, rows_operand, signs, w
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(7)
+
 import bit_quantized_linear_rotate_amd as w4  # noqa: E402
 
 
