@@ -32,6 +32,8 @@ CASES = {
     "tile256": ([256, 2049, 0, 513, 1, 700], 1),
     "large": ([700, 1, 900, 333, 0, 513, 64], 5),
     "largest": ([2600, 1, 2049, 513], 2),
+    # (a workgroup's tiles change between ones with rows in the lower half alone and full ones)
+    "few and many": ([3, 64, 40, 0, 33, 1, 64, 17] * 8, 2),
     "many experts": ([i % 3 for i in range(90)], 0),
     "nothing routed": ([0, 0, 0], 7),
 }
@@ -193,7 +195,9 @@ def check_route(l, k, **how):
 
 ROUTES = [(1, 1, 1, 1, 1), (1, 4, 2, 1, 1), (3, 8, 8, 1, 1), (32, 32, 4, 4, 2), (65, 64, 6, 8, 3), (300, 128, 8, 1, 1),
           (40, 160, 6, 8, 3), (129, 256, 8, 8, 4), (70, 256, 16, 64, 17), (50, 256, 20, 4, 2), (33, 384, 8, 16, 5),
-          (17, 1024, 32, 64, 9), (1500, 48, 3, 6, 2), (20, 12, 12, 12, 12), (30, 20, 3, 5, 3)]
+          (17, 1024, 32, 64, 9), (1500, 48, 3, 6, 2), (20, 12, 12, 12, 12), (30, 20, 3, 5, 3),
+          # as many choices as lanes leave room for, one more, and all experts
+          (40, 200, 14, 1, 1), (40, 200, 15, 1, 1), (20, 14, 14, 1, 1), (21, 16, 16, 4, 4)]
 
 
 @pytest.mark.parametrize("T,E,k,groups,top_groups", ROUTES)
