@@ -345,10 +345,13 @@ __device__ __forceinline__ void fp8_put_gated(const Fp8GemmArgs& a, v4f (&acc)[B
 // stores, 11.5 us with its beginning, which the next tile's products do not overlap.
 // Grouped, 32768 rows of 32 experts, K 1280, N 3840: 201 us in 16 bits, 260 in fp32 (503
 // MB of stores from ten steps a tile: 40 us less without them).
-// fp16 products: 8192 x 8192 x 8192 in fp32 920 us = 1.2 PFLOP/s, gated 32768 x 3840 x
-// 2560 598 = 1.08, the matrix cores busy half the time and the conversions most of the
-// rest (a bf16 product of the library: 1.46 to 1.49).  Converting a fragment while the
-// one before it multiplies, or two column tiles' products in turn, changed nothing.
+// fp16 products: 8192 x 8192 x 8192 in fp32 920 to 1010 us = 1.1 to 1.2 PFLOP/s, zeros
+// 845, gated 32768 x 3840 x 2560 598 = 1.08, the matrix cores busy half the time (a bf16
+// product of the library: 1.46 to 1.49).  Of 1010 us a quarter of the MFMAs is worth
+// 143, the conversions nothing (1010 without them): the rest is what a step of 128 rows
+// costs beside its MFMAs.  Fragments converted one product ahead, two column tiles'
+// MFMAs in turn, and the next step's weights read half a step earlier (at a second
+// meeting) gave the same time to 7% more.
 template <int BM, bool GROUPED, bool GATED, bool HALF>
 __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int tiles_m, int tiles_n)
 {
@@ -648,9 +651,9 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8GemmArgs a, int til
                 ssl = snx;
             }
         };
-        // Few rows: where a wave's are all past the tile's it only moves data (converting
-        // weights to fp16 costs as much as their products: 32 experts of 3840 x 2560 with
-        // two rows each, gated: 75 -> 66 us).
+        // Few rows: where a wave's are all past the tile's it only moves data, and leaves
+        // its SIMD to the wave of the other half (32 experts of 3840 x 2560 with two rows
+        // each, gated: 75 -> 66 us).
         if constexpr (HALF && BM == 64) {
             if (wm * (BM / 2) < cur.rows) steps(std::true_type{});
             else steps(std::false_type{});
