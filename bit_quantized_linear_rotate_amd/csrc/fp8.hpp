@@ -46,7 +46,7 @@ struct Fp8GemmArgs {
     int bias_dtype;
     void* out;                     // (M, N), or (R, N)
     int out_dtype;
-    bool half = false;             // products on the fp16 matrix cores: sums as exact as fp32 outputs
+    bool half = false;             // products on the fp16 matrix cores, for fp32 outputs and (always) gated ones
     // grouped by expert (E > 0): sorted row i of [offsets[e], offsets[e + 1])
     // is row rows[i] of a (row i where rows is null)
     int E = 0;

@@ -724,6 +724,8 @@ template <int BM, bool HALF> hipError_t launch_tile(const Fp8GemmArgs& a, hipStr
         hipLaunchKernelGGL((fp8_tile_kernel<BM, true, false, HALF>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
     else if constexpr (HALF)
         hipLaunchKernelGGL((fp8_tile_kernel<BM, true, true, true>), dim3(grid), dim3(512), 0, st, a, 0, (int)tn);
+    else
+        return hipErrorNotSupported;   // (gated products are fp16 ones)
     return hipGetLastError();
 }
 
