@@ -18,6 +18,7 @@
 
 #include "common.hpp"
 #include "mx4.hpp"
+#include "route_bounds.hpp"
 
 namespace w4a4 {
 
@@ -401,8 +402,7 @@ template <int L> __device__ __forceinline__ float lanes_maxf(float v)
 // and its index (i L + lane), the lower of equals: the index in the last BITS bits,
 // above it the value.  16-bit values (exact) fit as they are; others in fixed point
 // between the token's smallest and largest.  Then values `apart` units and less from
-// one another may be in either order: error (of their difference), and a unit each for
-// the difference, the product and the cut, of either.
+// one another may be in either order (error: of their difference).
 template <int L, int N, int BITS> struct Ranked {
     uint32_t key[N];
     uint32_t apart = 0;
@@ -421,11 +421,11 @@ template <int L, int N, int BITS> struct Ranked {
         hi = lanes_maxf<L>(hi);
         lo = -lanes_maxf<L>(-lo);
         const float range = add_rn(hi, -lo);
-        float unit = ((float)(1u << (32 - BITS)) - 512.0f) / range;
+        float unit = route_units(BITS) / range;
         if (!exact && hi > none) {
             // (a range of zero or infinity: nothing is told apart)
             if (!(unit < 0x1p120f && unit > 0.0f)) unit = 0.0f;
-            apart = (uint32_t)fminf(__builtin_fmaf(error, unit, 6.0f), 0x1p31f);
+            apart = route_apart(BITS, error, unit);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -460,15 +460,7 @@ template <int L, int N, int BITS> struct Ranked {
 
 // One token in fp32 by L lanes, NV consecutive experts each: choice r ends in lane r
 // (worth: its E values in LDS, sixteen and a gap each time, GROUPS only).
-// unsure: two values that decide who is chosen lie within their error.  exp(x) is off by
-// (1.5 |x| + 2) 2^-24 of itself (two roundings of its argument in base 2, the power),
-// 1 / (1 + exp(-l)) by s (1 - s) times that, at most 0.53 2^-24, or where all logits are
-// below zero (1.5 |l| + 2) 2^-24 of itself, and 3 2^-24 of itself for sum and
-// reciprocal; softmax terms by 3 2^-24 of the largest, their sum by NV + 6 and its
-// reciprocal and the product by 2; the bias adds 2^-24.  With V the largest of all scores
-// and choice values two choice values so differ by 2^-23 (6 + 1.5 |l|) V and 2^-23 (14 +
-// NV) V at most from their true difference, sums of two by twice that.  (2^-119: what
-// the hardware's reciprocal rounds to zero.)
+// unsure: two values that decide who is chosen lie within their error (route_bounds.hpp).
 template <int DT, int L, int NV, bool GROUPS>
 __device__ __forceinline__ void route_quick_token(const RouteScoredArgs& a, int64_t t, bool live, int lane, float* worth,
                                                   int& expert, float& weight, bool& unsure)
@@ -491,7 +483,7 @@ __device__ __forceinline__ void route_quick_token(const RouteScoredArgs& a, int6
     // scores, where the choice needs them; the sum of the softmax in double precision
     // where the candidates' values or the weights need it
     const bool sums = GROUPS && a.group_best == 2, scored = a.bias || sums;
-    float score[NV], error = 0.0f;   // of any choice value that is compared
+    float score[NV], error = 0.0f, sum_error = 0.0f;   // of a difference of choice values, of sums of two
     double total = 0.0;
     if (!a.sigmoid && (a.bias || !a.renormalize)) {
         // (a loop over memory: exp NV times over would fill the instruction cache)
@@ -528,7 +520,9 @@ __device__ __forceinline__ void route_quick_token(const RouteScoredArgs& a, int6
             }
             largest = fmaxf(largest, fmaxf(score[i], v));
         }
-        error = __builtin_fmaf(lanes_maxf<L>(largest), (a.sigmoid ? 6.0f - 1.5f * fminf(top, 0.0f) : 14.0f + NV) * 0x1p-23f, 0x1p-119f);
+        largest = lanes_maxf<L>(largest);
+        error = route_error(a.sigmoid, NV, top, largest);
+        sum_error = route_sum_error(error, largest);
         unsure = top == __builtin_inff();
     } else {
         unsure = false;
@@ -567,7 +561,7 @@ __device__ __forceinline__ void route_quick_token(const RouteScoredArgs& a, int6
         }
         __builtin_amdgcn_wave_barrier();
         Ranked<L, GN, 6> groups;
-        groups.set(of, !scored && narrow, scored ? 2.0f * error : 0.0f, lane);
+        groups.set(of, !scored && narrow, sums ? sum_error : error, lane);
         unsigned long long kept = 0;
         uint32_t last = 0;
         for (int r = 0; r < a.top_groups; ++r) {
