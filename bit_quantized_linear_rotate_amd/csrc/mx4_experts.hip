@@ -556,7 +556,9 @@ __device__ __forceinline__ void route_quick_token(const RouteScoredArgs& a, int6
                     for (int y = 0; y < 8; ++y) take(v[y]);
                 }
                 for (; x < size; ++x) take(worth[place(g * size + x)]);
-                of[i] = sums && m2 > none ? add_rn(m1, m2) : m1;
+                // (two of the lowest values: a worth all the same, and so far from the others
+                // that the choice goes to double precision)
+                of[i] = sums && m2 > none ? fmaxf(add_rn(m1, m2), -__FLT_MAX__) : m1;
             }
         }
         __builtin_amdgcn_wave_barrier();

@@ -274,3 +274,23 @@ def test_route_many_tokens(E, k, groups, top_groups, scores):
         assert torch.equal(rows.long(), slots // k)
         assert torch.equal(pos.flatten().long()[slots], torch.arange(T * k, device="cuda"))
         assert torch.equal(off.long()[1:], torch.bincount(flat, minlength=E).cumsum(0)) and int(off[0]) == 0
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", [(32, 8, 6, 8), (64, 8, 5, 14), (128, 16, 9, 14), (256, 8, 4, 20)])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_route_biases_of_the_lowest_value(E, groups, top_groups, k, scores):
+    """Experts put last by a bias of the type's lowest value, whole groups of them: the sum
+    of a group's two largest is below what fp32 holds, yet a group with such a worth comes
+    before one in which nothing can be taken."""
+    from tests.test_gpu_fp8_experts import check_route
+    need_gpu()
+    size, low = E // groups, torch.finfo(torch.float32).min
+    l = torch.randn(40, E, device="cuda")
+    l[::3, 3 * size:4 * size] = -float("inf")            # a group with nothing to take
+    bias = torch.full((E,), low, device="cuda")
+    bias[size], bias[2 * size + 1], bias[-1] = 0.25, 0.5, -0.25
+    for b in (bias, bias / 2, torch.full_like(bias, low), -bias):
+        for best in (1, 2):
+            for renormalize in (True, False):
+                check_route(l, k, scores=scores, bias=b, groups=groups, top_groups=top_groups, group_best=best,
+                            renormalize=renormalize)
