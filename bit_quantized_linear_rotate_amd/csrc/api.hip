@@ -284,7 +284,7 @@ ExpertsSpace experts_mx4_space(int64_t T, int64_t K, int64_t F, int E, int k, in
 // ---- block-scaled fp8 arguments --------------------------------------------
 constexpr int64_t kFp8MaxK = (int64_t)1 << 22;       // 256 rows of codes span at most 1 GB
 constexpr int64_t kFp8MaxRows = (int64_t)1 << 28;
-constexpr int kFp8MaxExperts = 16384;                // a grid of their row tiles stays below 2^16
+constexpr int kFp8MaxExperts = 16384;                // every workgroup of a grouped product reads their offsets
 
 int fp8_shape(int64_t rows, int64_t K, const char* what)
 {
@@ -346,8 +346,10 @@ int fp8_gemm_validate(const Fp8GemmArgs& a)
         return fail(W4A4_UNSUPPORTED, "unknown dtype code");
     const int64_t rows = a.E ? a.R : a.M;
     if (rows > 0 && a.N > 0 && !gated && !a.out) return fail(W4A4_INVALID, "out is NULL");
-    // tiles of 64 rows and 256 columns at the least: the grid stays below 2^31 threads
-    if ((rows / 64 + a.E + 1) * (a.N / 128 + 1) >= (int64_t)1 << 22)
+    // 2^28 - 32 columns by 32 of a workgroup of 512 (skinny kernel): less than 2^32 threads.
+    // Tiles of 64 rows by 256 columns, or 128 results, at the least: their number fits an int.
+    if (a.N > kFp8MaxRows - 32) return fail(W4A4_UNSUPPORTED, "N=%lld: at most 2^28 - 32", (long long)a.N);
+    if ((rows / 64 + a.E + 1) * (a.N / 128 + 1) >= (int64_t)1 << 30)
         return fail(W4A4_UNSUPPORTED, "an output of %lld x %lld is too large for one call", (long long)rows, (long long)a.N);
     return W4A4_OK;
 }

@@ -452,10 +452,12 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
  *   the block, scale = A / 448, code = e4m3(448 y / A) to nearest, ties to the even
  *   code (the product and the quotient each in fp32); a block that holds a NaN or an
  *   infinity gets the scale NaN and codes 0.  K is a multiple of 16, at most 2^22; at
- *   most 2^28 rows.  The products refuse (W4A4_UNSUPPORTED) activations of more than
- *   2^31 bytes of scales, codes of more than 2^31 bytes behind a row index (so the
- *   expert layer's x), more than 16384 experts, grouped outputs of 2^23 bytes a row
- *   and more, and outputs of R x N (M x N) with (R / 64 + E + 1) (N / 128 + 1) >= 2^22.
+ *   most 2^28 rows; the quantisers refuse (W4A4_UNSUPPORTED) (rows / 16 + 1) (K / 256 + 1)
+ *   times E of 2^24 and more.  The products refuse activations of more than 2^31 bytes
+ *   of scales, codes of more than 2^31 bytes behind a row index (so the expert layer's
+ *   x), more than 16384 experts, weights of more than 2^28 - 32 rows, grouped outputs of
+ *   2^23 bytes a row and more, and outputs of R x N (M x N) with (R / 64 + E + 1)
+ *   (N / 128 + 1) >= 2^30.
  *
  * w8a8_quantize_fp8: rows of x (any strides; 16-byte aligned contiguous rows take
  *   wide loads), rotated first if g > 0, as for w4a4_quantize_mx4.

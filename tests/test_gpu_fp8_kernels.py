@@ -115,6 +115,22 @@ def test_many_dense_tiles_a_workgroup(out, M, N):
         assert torch.equal(got[m:m + (1 << 16)], (av[m:m + (1 << 16)].float() @ wt).to(DT[out])), m
 
 
+def test_an_output_of_64_gb():
+    """2^20 x 32768 bf16: offsets past 2^35, 2048 tiles for each workgroup."""
+    need_gpu()
+    M, K, N = 1 << 20, 16, 1 << 15
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("less than 100 GB of free memory")
+    a, sa, av = rows_of_ints(M, K)
+    w, sw, wv = weights_of_ints(N, K)
+    got = w4.w8a8_gemm_fp8(a, sa, w[0], sw[0])
+    wt = wv[0].float().t().contiguous()
+    for m in range(0, M, 1 << 14):
+        assert torch.equal(got[m:m + (1 << 14)], (av[m:m + (1 << 14)].float() @ wt).bfloat16()), m
+    del got
+    torch.cuda.empty_cache()
+
+
 def test_many_grouped_tiles_a_workgroup():
     """16384 experts of one or two rows, three column tiles each; the gated product
     against the same experts in eight calls of few tiles."""
