@@ -1682,7 +1682,9 @@ def w8a8_experts_fp8(x: torch.Tensor, logits: torch.Tensor, top_k: int, w13_code
     route (as w4a4_route_experts_scored), quantize (rotated by h first if given), gated
     product with w13 (E, 2 F, K; F gates then F ups, F % 128 == 0), product with w2 (E,
     K, F), weighted sum per token.  The experts' rows wait for the sum in rows_dtype:
-    float32, or x's (half the bytes, but a 16-bit layer then rounds twice)."""
+    float32, or x's (half the bytes, but a 16-bit layer then rounds twice).  The product
+    with w2 is the fp8 matrix core's unless x is float32; w8a8_grouped_gemm_fp8 takes
+    the fp16 core for float32 outputs."""
     lead = _need(x, "x", contiguous=False).shape[:-1]
     x2 = _as_2d(x)
     T, K = x2.shape

@@ -467,10 +467,12 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
  * w8a8_dequantize_fp8, w8a8_dequantize_weights_fp8: the values in out_dtype (code
  *   times scale in fp32, rounded once more to 16 bits), 16-byte aligned.
  * w8a8_gemm_fp8: out[m][n] = O(sum_b sa[b][m] sw[n/128][b] (sum_{k in b} a[m][k]
- *   w[n][k]) + bias[n]), fp32 sums, the inner ones on the matrix cores.
- *   The fp8 matrix core adds eight neighbouring products to 2^-13 of the largest
- *   (1.5e-5 of a sum of random rows); fp32 outputs and the gated product take the
- *   fp16 matrix core, half as fast, with sums as exact as fp32.
+ *   w[n][k]) + bias[n]), fp32 sums, the inner ones on the matrix cores, the two
+ *   scales' product in fp32 too.  The fp8 matrix core adds eight neighbouring products to
+ *   2^-13 of the largest (1.4e-5 of an output, rms over random rows; a few times that
+ *   where single k outweigh the others).  16-bit outputs of more rows than the skinny
+ *   kernel takes come from it.  fp32 outputs, the skinny kernel and the gated product
+ *   take the fp16 matrix core, half as fast, whose sums are those of fp32.
  * w8a8_linear_fp8: quantiser and product back to back; bias in x_dtype; a workspace
  *   of w8a8_linear_fp8_workspace_size(M, K) bytes, 16-byte aligned.
  * w8a8_grouped_gemm_fp8: sorted rows, offsets and row index as for
@@ -497,7 +499,10 @@ int w4a4_experts_mx4_rows(const void* x, int x_dtype, int64_t T, int64_t K, int6
  * w8a8_experts_fp8: w4a4_route_experts_scored, quantise, gated product (w13: (E, 2 F,
  *   K), gates first, F a multiple of 128), product (w2: (E, K, F)), combine; the
  *   experts' rows are kept in rows_dtype, W4A4_F32 or x_dtype (half the bytes; a
- *   16-bit layer then rounds twice).  No biases of the products; T * top_k < 2^28.  Workspace of
+ *   16-bit layer then rounds twice).  The second product takes the fp16 matrix core for
+ *   fp32 x and the fp8 one for 16-bit x, whatever rows_dtype is: there fp32 rows differ
+ *   from those of w8a8_grouped_gemm_fp8 with fp32 outputs by the fp8 core's sums.
+ *   No biases of the products; T * top_k < 2^28.  Workspace of
  *   w8a8_experts_fp8_workspace_size(.., rows_dtype) bytes, 16-byte aligned.
  */
 int w8a8_quantize_fp8(const void* x, int x_dtype, int64_t M, int64_t K, int64_t stride_m,
